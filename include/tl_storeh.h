@@ -69,7 +69,8 @@ typedef enum {
   TL_ERR_UNSUPPORTED = 4,    /* a shape the kernels are not built for (see tl_storeh_desc) */
   TL_ERR_CUDA = 5,           /* a CUDA runtime call or launch failed */
   TL_ERR_DEVICE_TIMEOUT = 6, /* a bounded wait inside a kernel gave up (recorded on the device) */
-  TL_ERR_DEVICE_RANGE = 7    /* a per-lane device value was out of range; that lane was skipped */
+  TL_ERR_DEVICE_RANGE = 7,   /* a per-lane device value was out of range; that lane was skipped */
+  TL_ERR_DEVICE_CAPACITY = 8 /* tl_paged_reserve (tl_paged.h): too few free pages; recorded on the device */
 } tl_status;
 
 /* How a cached h row is stored. */
@@ -405,8 +406,8 @@ TL_API tl_status tl_storeh_attn_decode_static_ws(const tl_storeh_desc* desc, tl_
  * Synchronises `stream`, then reads and clears the status word that kernels
  * of tl_storeh_attn_decode record in `workspace`.  Returns TL_OK,
  * TL_ERR_DEVICE_TIMEOUT (a bounded device wait gave up), TL_ERR_DEVICE_RANGE
- * (a lane's loops/ctx_len was out of range and the lane was skipped) or
- * TL_ERR_CUDA.  The status word starts at the beginning of the workspace,
+ * (a lane's loops/ctx_len was out of range and the lane was skipped),
+ * TL_ERR_DEVICE_CAPACITY (a paged cache ran out of free pages) or TL_ERR_CUDA.  The status word starts at the beginning of the workspace,
  * whose first 256 bytes are reserved for it; a freshly allocated workspace
  * must have those 256 bytes zero-filled once (or be cleared with this call)
  * before its first use.  When the word is not zero this call clears all 256

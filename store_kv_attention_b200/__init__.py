@@ -6,7 +6,8 @@ fallback: the first call fails loudly when the library is missing.
 
 The same names as the C ABI in ``include/tl_storeh.h``:
 ``cache_bytes``, ``workspace_bytes``, ``append``, ``attn_decode``,
-``residual_norm_check``, ``poll_status``.
+``residual_norm_check``, ``poll_status``; in ``include/tl_delta.h``: ``delta_*``; and in
+``include/tl_paged.h``, the paged cache of K and V: ``PagedDesc``, ``PagedCache``, ``paged_*``.
 """
 from __future__ import annotations
 
@@ -26,19 +27,26 @@ TL_ERR_UNSUPPORTED = 4
 TL_ERR_CUDA = 5
 TL_ERR_DEVICE_TIMEOUT = 6
 TL_ERR_DEVICE_RANGE = 7
+TL_ERR_DEVICE_CAPACITY = 8
 
 TL_H_FP16 = 0
 TL_H_INT8_TOKEN = 1
 TL_H_INT4_G64 = 2
 
-# every symbol include/tl_storeh.h declares
+TL_KV_FP16 = 0
+TL_KV_BF16 = 1
+
+# every symbol the headers declare
 EXPORTS = ["tl_storeh_cache_bytes", "tl_storeh_workspace_bytes", "tl_storeh_append", "tl_storeh_attn_decode",
            "tl_residual_norm_check", "tl_storeh_poll_status", "tl_status_string", "tl_last_error_message",
            "tl_storeh_abi_version", "tl_set_profile", "tl_storeh_attn_decode_static_ws",
            "tl_storeh_append_attn_decode", "tl_storeh_selftest_wait_timeout", "tl_delta_cache_bytes",
            "tl_delta_append", "tl_delta_workspace_bytes", "tl_delta_attn_decode", "tl_storeh_verify_attn",
            "tl_storeh_verify_workspace_bytes", "tl_storeh_prefill_attn", "tl_storeh_decode_ex",
-           "tl_storeh_workspace_bytes_ex", "tl_storeh_attn_decode_rope", "tl_storeh_rope_workspace_bytes"]
+           "tl_storeh_workspace_bytes_ex", "tl_storeh_attn_decode_rope", "tl_storeh_rope_workspace_bytes",
+           "tl_paged_cache_bytes", "tl_paged_workspace_bytes", "tl_paged_append", "tl_paged_attn_decode",
+           "tl_paged_prompt_attn", "tl_paged_copy", "tl_paged_fork", "tl_paged_reserve", "tl_paged_free",
+           "tl_paged_compact"]
 
 
 class TLError(RuntimeError):
@@ -73,6 +81,16 @@ class DeltaDescC(ctypes.Structure):
 
 class DeltaCacheC(ctypes.Structure):
     _fields_ = [("anchor", ctypes.c_void_p), ("deltas", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class PagedDescC(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("max_seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class PagedCacheC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p), ("refs", ctypes.c_void_p)]
 
 
 _lib_handle = None
@@ -137,6 +155,22 @@ def _load():
     L.tl_storeh_rope_workspace_bytes.argtypes = [P(Desc), i32, P(sz)]
     L.tl_storeh_rope_workspace_bytes.restype = ctypes.c_int
     L.tl_storeh_verify_workspace_bytes.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    L.tl_paged_cache_bytes.argtypes = [P(PagedDescC), P(sz), P(sz), P(sz)]
+    L.tl_paged_workspace_bytes.argtypes = [P(PagedDescC), i32, i32, i32, P(sz)]
+    L.tl_paged_append.argtypes = [P(PagedDescC), PagedCacheC, i32, vp, i64, vp, i64, i32, vp, vp, vp, i32, vp, sz, vp]
+    L.tl_paged_attn_decode.argtypes = [P(PagedDescC), PagedCacheC, i32, i32, vp, i64, vp, vp, f32, i32, vp, i32, vp, sz,
+                                       vp]
+    L.tl_paged_prompt_attn.argtypes = [P(PagedDescC), PagedCacheC, i32, i32, vp, i64, i32, vp, vp, vp, f32, vp, i32, vp,
+                                       sz, vp]
+    L.tl_paged_copy.argtypes = [P(PagedDescC), PagedCacheC, vp, vp, i32, vp, sz, vp]
+    L.tl_paged_fork.argtypes = [P(PagedDescC), PagedCacheC, vp, vp, vp, i32, vp, sz, vp]
+    L.tl_paged_reserve.argtypes = L.tl_paged_fork.argtypes
+    L.tl_paged_free.argtypes = [P(PagedDescC), PagedCacheC, vp, vp, i32, vp, sz, vp]
+    L.tl_paged_compact.argtypes = [P(PagedDescC), PagedCacheC, vp, vp, sz, vp]
+    for f in EXPORTS:
+        if f.startswith("tl_paged_"):
+            getattr(L, f).restype = ctypes.c_int
     _lib_handle = L
     return L
 
@@ -439,3 +473,177 @@ class ProfileHook:
     def stream_kernel_ms(self):
         """Durations (ms) of the bracketed streaming-kernel launches (call after a synchronize)."""
         return [b.elapsed_time(e) for b, e in self.events[: self.p.recorded]]
+
+
+# ---------------------------------------------------------------- paged cache of K and V (include/tl_paged.h)
+@dataclasses.dataclass
+class PagedDesc:
+    n_layers: int
+    n_pages: int
+    page_size: int
+    n_kv_heads: int
+    head_dim: int
+    max_seqs: int
+    max_pages: int
+    dtype: int = TL_KV_FP16
+
+    def c(self) -> PagedDescC:
+        return PagedDescC(self.n_layers, self.n_pages, self.page_size, self.n_kv_heads, self.head_dim, self.max_seqs,
+                          self.max_pages, self.dtype)
+
+
+def paged_cache_bytes(desc: PagedDesc):
+    """Bytes of k (and of v), of the page table and of the counts."""
+    p, t, r = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t()
+    _check(_load().tl_paged_cache_bytes(ctypes.byref(desc.c()), ctypes.byref(p), ctypes.byref(t), ctypes.byref(r)),
+           "tl_paged_cache_bytes")
+    return p.value, t.value, r.value
+
+
+def paged_workspace_bytes(desc: PagedDesc, n_heads: int, n_lanes: int, split_rows: int = 0) -> int:
+    b = ctypes.c_size_t()
+    _check(_load().tl_paged_workspace_bytes(ctypes.byref(desc.c()), n_heads, n_lanes, split_rows, ctypes.byref(b)),
+           "tl_paged_workspace_bytes")
+    return b.value
+
+
+class PagedCache:
+    """Device buffers of one paged cache: k, v [n_layers, n_pages, n_kv_heads, page_size, head_dim],
+    table int32 [max_seqs, max_pages] (-1), refs int32 [n_pages] (0) and a zeroed workspace for calls
+    of up to n_lanes lanes of n_heads query heads.  Buffers of the caller's own can be given instead."""
+
+    def __init__(self, desc: PagedDesc, n_heads: int, n_lanes: int, device="cuda", split_rows: int = 0, k=None, v=None,
+                 table=None, refs=None):
+        import torch
+        self.desc, self.n_heads, self.split_rows = desc, n_heads, split_rows
+        self.ws_bytes = paged_workspace_bytes(desc, n_heads, n_lanes, split_rows)
+        self.dtype = torch.float16 if desc.dtype == TL_KV_FP16 else torch.bfloat16
+        pool = (desc.n_layers, desc.n_pages, desc.n_kv_heads, desc.page_size, desc.head_dim)
+        rows = (desc.max_seqs, desc.max_pages)
+        if k is not None:
+            device = k.device
+        self.k = torch.empty(pool, dtype=self.dtype, device=device) if k is None else k
+        self.v = torch.empty(pool, dtype=self.dtype, device=device) if v is None else v
+        self.table = torch.full(rows, -1, dtype=torch.int32, device=device) if table is None else table
+        self.refs = torch.zeros(desc.n_pages, dtype=torch.int32, device=device) if refs is None else refs
+        self.device = self.k.device
+        for name, t, shape, dt in (("k", self.k, pool, self.dtype), ("v", self.v, pool, self.dtype),
+                                   ("table", self.table, rows, torch.int32), ("refs", self.refs, (desc.n_pages,), torch.int32)):
+            _paged_tensor(self, name, t, dt, shape)
+        self.workspace = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
+
+    def c(self) -> PagedCacheC:
+        return PagedCacheC(self.k.data_ptr(), self.v.data_ptr(), self.table.data_ptr(), self.refs.data_ptr())
+
+
+def _paged_tensor(cache: PagedCache, name: str, t, dtype, shape, rows: bool = False):
+    """Raises unless t lies on the cache's device with this type and shape (None: any extent) and is dense
+    (rows: only behind its first axis)."""
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, not {dtype}")
+    if t.dim() != len(shape) or any(w is not None and w != n for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple('n' if w is None else w for w in shape)}")
+    want = 1
+    for axis in reversed(range(1 if rows else 0, t.dim())):
+        if t.shape[axis] != 1 and t.stride(axis) != want:
+            raise ValueError(f"{name} is not dense: strides {t.stride()}")
+        want *= t.shape[axis]
+
+
+def _paged_rows(cache: PagedCache, name: str, t, heads: int) -> int:
+    """The row stride of [n, heads, head_dim] rows, which may be part of wider rows."""
+    _paged_tensor(cache, name, t, cache.dtype, (None, heads, cache.desc.head_dim), rows=True)
+    if t.shape[0] < 2:
+        return 0
+    if t.stride(0) <= 0:
+        raise ValueError(f"{name} has overlapping rows: strides {t.stride()}")
+    return t.stride(0)
+
+
+def _paged_ints(cache: PagedCache, n: int, **tensors) -> None:
+    import torch
+    for name, t in tensors.items():
+        if t is not None:
+            _paged_tensor(cache, name, t, torch.int32, (n,))
+
+
+def _paged_call(cache: PagedCache, name: str, args, stream) -> None:
+    """Calls name(desc, cache, *args, workspace, its size, stream) with the cache's device current."""
+    import torch
+    with torch.cuda.device(cache.device):
+        _check(getattr(_load(), name)(ctypes.byref(cache.desc.c()), cache.c(), *args, cache.workspace.data_ptr(),
+                                      cache.ws_bytes, _stream(stream)), name)
+
+
+def paged_append(cache: PagedCache, layer: int, k_rows, v_rows, start_pos, cu_rows=None, seqs=None, stream=None) -> None:
+    """tl_paged_append: k_rows, v_rows [n, n_kv_heads, head_dim] in the cache's type (rows may be strided);
+    start_pos / seqs int32 [n_lanes], cu_rows int32 [n_lanes + 1] (None: one row per lane)."""
+    ks = _paged_rows(cache, "k_rows", k_rows, cache.desc.n_kv_heads)
+    vs = _paged_rows(cache, "v_rows", v_rows, cache.desc.n_kv_heads)
+    if k_rows.shape[0] != v_rows.shape[0]:
+        raise ValueError(f"{k_rows.shape[0]} rows of K, {v_rows.shape[0]} of V")
+    n = int(start_pos.numel())
+    _paged_ints(cache, n, start_pos=start_pos, seqs=seqs)
+    _paged_ints(cache, n + 1, cu_rows=cu_rows)
+    _paged_call(cache, "tl_paged_append", (layer, _ptr(k_rows), ks, _ptr(v_rows), vs, int(k_rows.shape[0]), _ptr(cu_rows),
+                                           _ptr(start_pos), _ptr(seqs), n), stream)
+
+
+def paged_attn_decode(cache: PagedCache, layer: int, q, kv_len, out, seqs=None, scale: float = 0.0, stream=None) -> None:
+    """tl_paged_attn_decode: q [n_lanes, n_heads, head_dim] (rows may be strided), kv_len / seqs int32 [n_lanes],
+    out [n_lanes, n_heads, head_dim]; scale 0: 1 / sqrt(head_dim).  Splits of cache.split_rows positions."""
+    n, heads = int(q.shape[0]), int(q.shape[1])
+    qs = _paged_rows(cache, "q", q, heads)
+    _paged_tensor(cache, "out", out, cache.dtype, (n, heads, cache.desc.head_dim))
+    _paged_ints(cache, n, kv_len=kv_len, seqs=seqs)
+    _paged_call(cache, "tl_paged_attn_decode", (layer, heads, _ptr(q), qs, _ptr(kv_len), _ptr(seqs), float(scale),
+                                                cache.split_rows, _ptr(out), n), stream)
+
+
+def paged_prompt_attn(cache: PagedCache, layer: int, q, cu_q, kv_len, out, seqs=None, scale: float = 0.0,
+                      stream=None) -> None:
+    """tl_paged_prompt_attn: packed queries q [n, n_heads, head_dim] (rows may be strided), cu_q int32
+    [n_lanes + 1], kv_len / seqs int32 [n_lanes], out [n, n_heads, head_dim]."""
+    n, heads, lanes = int(q.shape[0]), int(q.shape[1]), int(kv_len.numel())
+    qs = _paged_rows(cache, "q", q, heads)
+    _paged_tensor(cache, "out", out, cache.dtype, (n, heads, cache.desc.head_dim))
+    _paged_ints(cache, lanes, kv_len=kv_len, seqs=seqs)
+    _paged_ints(cache, lanes + 1, cu_q=cu_q)
+    _paged_call(cache, "tl_paged_prompt_attn", (layer, heads, _ptr(q), qs, n, _ptr(cu_q), _ptr(kv_len), _ptr(seqs),
+                                                float(scale), _ptr(out), lanes), stream)
+
+
+def paged_copy(cache: PagedCache, src, dst, stream=None) -> None:
+    """tl_paged_copy: page src[i] to page dst[i] (int32 [n], device), every layer's K and V."""
+    n = int(src.numel())
+    _paged_ints(cache, n, src=src, dst=dst)
+    _paged_call(cache, "tl_paged_copy", (_ptr(src), _ptr(dst), n), stream)
+
+
+def paged_fork(cache: PagedCache, src, dst, n_tokens, stream=None) -> None:
+    """tl_paged_fork: sequence dst[i] shares the first n_tokens[i] positions of src[i] (int32 [n], device)."""
+    n = int(src.numel())
+    _paged_ints(cache, n, src=src, dst=dst, n_tokens=n_tokens)
+    _paged_call(cache, "tl_paged_fork", (_ptr(src), _ptr(dst), _ptr(n_tokens), n), stream)
+
+
+def paged_reserve(cache: PagedCache, seqs, ctx_len, n_new, stream=None) -> None:
+    """tl_paged_reserve: pages of its own for positions ctx_len[i] .. + n_new[i] - 1 of sequence seqs[i]."""
+    n = int(seqs.numel())
+    _paged_ints(cache, n, seqs=seqs, ctx_len=ctx_len, n_new=n_new)
+    _paged_call(cache, "tl_paged_reserve", (_ptr(seqs), _ptr(ctx_len), _ptr(n_new), n), stream)
+
+
+def paged_free(cache: PagedCache, seqs, keep=None, stream=None) -> None:
+    """tl_paged_free: the pages behind the first keep[i] positions (None: all) of sequence seqs[i]."""
+    n = int(seqs.numel())
+    _paged_ints(cache, n, seqs=seqs, keep=keep)
+    _paged_call(cache, "tl_paged_free", (_ptr(seqs), _ptr(keep), n), stream)
+
+
+def paged_compact(cache: PagedCache, n_live=None, stream=None) -> None:
+    """tl_paged_compact: the pages in use become pages 0 .. n - 1; n_live (int32 [1]) receives n."""
+    _paged_ints(cache, 1, n_live=n_live)
+    _paged_call(cache, "tl_paged_compact", (_ptr(n_live),), stream)

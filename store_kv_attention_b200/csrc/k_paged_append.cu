@@ -1,0 +1,101 @@
+// Rows of K and V into the paged cache (tl_paged_append).
+//
+// A copy: row r of the packed input, [kv][hd] of K and of V, goes to the page of its position, one
+// run of hd values per K/V head.  Bytes (2 x 2 x n_rows x kv x hd x 2) bound it; a call of single
+// tokens is bound by its chain of dependent loads (cu_rows, start_pos, table, refs, then the rows).
+// One warp takes 2 KB of K or of V of one row, so that a lane has four 16-byte loads in flight and a
+// 48-token call still spreads over as many warps as it has parts.
+#include "paged_internal.cuh"
+#include "tc_ptx.cuh"
+
+namespace tl {
+namespace {
+
+constexpr int kAppendThreads = 256;
+constexpr int kPart = 128;  // 16-byte chunks of one row a warp takes at a time
+
+// The lane that owns packed row r: the largest b with cu[b] <= r, for cu[0] <= r < cu[n].  All lanes
+// of the warp search together, 32 bounds a step.  Any contents of cu give a b in [0, n).
+__device__ __forceinline__ int find_lane(const int32_t* cu, int n, int r, int lane) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, at < hi && (lane == 0 || cu[at] <= r));
+    lo += (31 - __clz(le)) * step;
+    hi = lo + step < hi ? lo + step : hi;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kAppendThreads)
+    paged_append_kernel(PagedShape s, PagedBufs c, size_t layer_off, const uint16_t* k_rows, int64_t k_stride,
+                        const uint16_t* v_rows, int64_t v_stride, int n_rows, const int32_t* cu_rows,
+                        const int32_t* start_pos, const int32_t* seqs, int n_lanes, uint32_t* status) {
+  ptx::pdl_wait();
+  ptx::pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int chunks = s.kv * s.hd / 8, parts = (chunks + kPart - 1) / kPart;
+  const int per_head = s.hd / 8;
+  const long long units = (long long)n_rows * parts * 2;
+  const long long step = (long long)gridDim.x * (kAppendThreads / 32);
+  int first = 0, last = n_rows;
+  if (cu_rows) {
+    first = cu_rows[0];
+    last = cu_rows[n_lanes];
+  }
+  for (long long u = (long long)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5); u < units; u += step) {
+    const bool is_v = u & 1;
+    const int part = (int)((u >> 1) % parts), r = (int)((u >> 1) / parts);
+    if (r < first || r >= last) continue;
+    // the row's values are on their way while its place is looked up
+    const uint4* src = reinterpret_cast<const uint4*>(is_v ? v_rows + r * v_stride : k_rows + r * k_stride);
+    uint4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = part * kPart + i * 32 + lane;
+      if (at < chunks) x[i] = __ldg(src + at);
+    }
+    const int b = cu_rows ? find_lane(cu_rows, n_lanes, r, lane) : r;
+    const int seq = seqs ? seqs[b] : b;
+    const long long pos = (long long)start_pos[b] + (cu_rows ? r - cu_rows[b] : 0);
+    bool ok = seq >= 0 && seq < s.max_seqs && pos >= 0 && pos < s.max_len();
+    int page = -1;
+    if (ok) page = c.table[(size_t)seq * s.max_pages + (int)(pos / s.page)];
+    ok = ok && page >= 0 && page < s.n_pages;
+    if (ok && c.refs) ok = c.refs[page] <= 1;
+    if (!ok) {
+      if (lane == 0) atomicOr(status, kStatusRange);
+      continue;
+    }
+    uint16_t* dst = (is_v ? c.v : c.k) + layer_off + (size_t)page * s.page_elems() + (size_t)(pos % s.page) * s.hd;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = part * kPart + i * 32 + lane;
+      if (at < chunks) *reinterpret_cast<uint4*>(dst + (size_t)(at / per_head) * s.block_elems() + (at % per_head) * 8) = x[i];
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedShape& s, const PagedBufs& c, int layer, const void* k_rows, int64_t k_stride,
+                                const void* v_rows, int64_t v_stride, int n_rows, const int32_t* cu_rows,
+                                const int32_t* start_pos, const int32_t* seqs, int n_lanes, uint32_t* status,
+                                cudaStream_t st) {
+  const long long units = (long long)n_rows * ((s.kv * s.hd / 8 + kPart - 1) / kPart) * 2;
+  const long long blocks = (units + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = st;
+  cfg.gridDim = dim3((unsigned)(blocks < 148 * 8 ? blocks : 148 * 8));
+  cfg.blockDim = dim3(kAppendThreads);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, paged_append_kernel, s, c, (size_t)layer * s.layer_elems(),
+                                     (const uint16_t*)k_rows, k_stride, (const uint16_t*)v_rows, v_stride, n_rows,
+                                     cu_rows, start_pos, seqs, n_lanes, status);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace tl

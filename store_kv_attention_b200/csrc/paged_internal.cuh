@@ -1,0 +1,137 @@
+// Internal declarations of the paged K/V cache (include/tl_paged.h): shape, workspace layout and
+// launchers.
+#pragma once
+
+#include "tl_internal.cuh"
+#include "tl_paged.h"
+
+namespace tl {
+
+constexpr int kPagedMaxLanes = 1024;  // lanes (sequences) per call: the plans keep one word per lane in shared memory
+
+struct PagedShape {
+  int layers, n_pages, page, kv, hd, max_seqs, max_pages, dtype;
+  __host__ __device__ size_t block_elems() const { return (size_t)page * hd; }           // one (page, K/V head)
+  __host__ __device__ size_t page_elems() const { return (size_t)kv * page * hd; }       // one page of a layer
+  __host__ __device__ size_t layer_elems() const { return (size_t)n_pages * page_elems(); }
+  __host__ __device__ int max_len() const { return max_pages * page; }
+};
+
+// The cache's buffers as the kernels take them.
+struct PagedBufs {
+  uint16_t* k;
+  uint16_t* v;
+  int32_t* table;
+  int32_t* refs;
+};
+
+// Splits of one lane's `len` positions: target = the splits a lane should have so that the call
+// fills the GPU (0: splits of `fixed` positions).  Otherwise at least ceil(len / kSplitMost)
+// splits, at most one per kSplitLeast positions, of equal length rounded up to 64 positions.
+constexpr int kSplitLeast = 128, kSplitMost = 2048;
+__host__ __device__ inline int paged_split_rows(int len, int target, int fixed) {
+  if (target == 0) return fixed;
+  const int fine = (len + kSplitLeast - 1) / kSplitLeast, coarse = (len + kSplitMost - 1) / kSplitMost;
+  int n = fine < target ? fine : target;
+  n = n > coarse ? n : coarse;
+  n = n > 1 ? n : 1;
+  const int rows = (len + n - 1) / n;
+  return rows <= 64 ? 64 : (rows + 63) / 64 * 64;
+}
+__host__ __device__ inline int paged_splits(int len, int target, int fixed) {
+  const int rows = paged_split_rows(len, target, fixed);
+  return len <= rows ? 1 : (len + rows - 1) / rows;
+}
+
+// Workspace: status word | per-split (max, sum) and unnormalised sums of the decode; the plan of the
+// operations on pages (counters | moves: source, destination | one word per page) lies over them.
+struct PagedWorkspace {
+  size_t ml_off, acc_off, total;  // decode
+  int s_max, target;              // splits a lane can have; paged_split_rows' target
+};
+// K/V heads times tiles of 16 query heads: the CTAs that one split of one lane takes.
+inline int paged_tiles(const PagedShape& s, int n_heads) { return s.kv * ((n_heads / s.kv + 15) / 16); }
+constexpr int kPagedSlots = 296;  // two CTAs on each of the 148 SMs
+inline PagedWorkspace paged_workspace(const PagedShape& s, int n_heads, int n_lanes, int split_rows) {
+  PagedWorkspace w;
+  const int pairs = n_lanes * paged_tiles(s, n_heads), len = s.max_len();
+  const int fine = (len + kSplitLeast - 1) / kSplitLeast, coarse = (len + kSplitMost - 1) / kSplitMost;
+  w.target = split_rows ? 0 : (kPagedSlots + pairs - 1) / pairs;
+  w.s_max = w.target < fine ? w.target : fine;
+  if (w.s_max < coarse) w.s_max = coarse;
+  if (split_rows) w.s_max = (len + split_rows - 1) / split_rows;
+  const size_t parts = (size_t)n_lanes * n_heads * w.s_max;
+  w.ml_off = 256;
+  w.acc_off = align256(w.ml_off + parts * 8);
+  w.total = align256(w.acc_off + parts * s.hd * 4);
+  return w;
+}
+// Enough for every call of up to n_lanes lanes: with fewer lanes a lane has more splits, but
+// n * ceil(slots / (n * tiles)) never passes slots / tiles + n.
+inline size_t paged_workspace_upto(const PagedShape& s, int n_heads, int n_lanes, int split_rows) {
+  const size_t fine = (s.max_len() + kSplitLeast - 1) / kSplitLeast, coarse = (s.max_len() + kSplitMost - 1) / kSplitMost;
+  size_t lane_splits = kPagedSlots / paged_tiles(s, n_heads) + 1 + (size_t)n_lanes;
+  if (lane_splits > n_lanes * fine) lane_splits = n_lanes * fine;
+  if (lane_splits < n_lanes * coarse) lane_splits = n_lanes * coarse;
+  if (split_rows) lane_splits = n_lanes * (size_t)((s.max_len() + split_rows - 1) / split_rows);
+  const size_t parts = lane_splits * n_heads;
+  return align256(align256(256 + parts * 8) + parts * s.hd * 4);
+}
+struct PagedOpsWorkspace {
+  size_t count_off, moves_off, list_off, total;
+};
+inline PagedOpsWorkspace paged_ops_workspace(const PagedShape& s) {
+  PagedOpsWorkspace w;
+  w.count_off = 256;
+  w.moves_off = 512;
+  w.list_off = align256(w.moves_off + (size_t)s.n_pages * 8);
+  w.total = align256(w.list_off + (size_t)s.n_pages * 4);
+  return w;
+}
+
+struct PagedDecodeArgs {
+  PagedShape s;
+  PagedBufs c;
+  int layer, n_heads, n_lanes, split_rows;
+  const void* q;
+  int64_t q_stride;
+  const int32_t* kv_len;
+  const int32_t* seqs;
+  float scale;
+  void* out;
+  uint8_t* ws;
+  PagedWorkspace wl;
+};
+struct PagedPromptArgs {
+  PagedShape s;
+  PagedBufs c;
+  int layer, n_heads, n_lanes, n_rows;
+  const void* q;
+  int64_t q_stride;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  const int32_t* seqs;
+  float scale;
+  void* out;
+  uint8_t* ws;
+};
+
+cudaError_t launch_paged_append(const PagedShape& s, const PagedBufs& c, int layer, const void* k_rows, int64_t k_stride,
+                                const void* v_rows, int64_t v_stride, int n_rows, const int32_t* cu_rows,
+                                const int32_t* start_pos, const int32_t* seqs, int n_lanes, uint32_t* status,
+                                cudaStream_t st);                                       // k_paged_append.cu
+cudaError_t launch_paged_decode(const PagedDecodeArgs& a, cudaStream_t st);             // k_paged_decode.cu
+cudaError_t launch_paged_prompt(const PagedPromptArgs& a, cudaStream_t st);             // k_paged_prompt.cu
+// k_paged_pages.cu
+cudaError_t launch_paged_copy(const PagedShape& s, const PagedBufs& c, const int32_t* src, const int32_t* dst, int n,
+                              uint8_t* ws, cudaStream_t st);
+cudaError_t launch_paged_fork(const PagedShape& s, const PagedBufs& c, const int32_t* src, const int32_t* dst,
+                              const int32_t* n_tokens, int n, uint8_t* ws, cudaStream_t st);
+cudaError_t launch_paged_reserve(const PagedShape& s, const PagedBufs& c, const int32_t* seqs, const int32_t* ctx_len,
+                                 const int32_t* n_new, int n, uint8_t* ws, cudaStream_t st);
+cudaError_t launch_paged_free(const PagedShape& s, const PagedBufs& c, const int32_t* seqs, const int32_t* keep, int n,
+                              uint8_t* ws, cudaStream_t st);
+cudaError_t launch_paged_compact(const PagedShape& s, const PagedBufs& c, int32_t* n_live, uint8_t* ws,
+                                 cudaStream_t st);
+
+}  // namespace tl

@@ -177,6 +177,7 @@ const char* tl_status_string(tl_status st) {
     case TL_ERR_CUDA: return "TL_ERR_CUDA: a CUDA call failed";
     case TL_ERR_DEVICE_TIMEOUT: return "TL_ERR_DEVICE_TIMEOUT: a bounded device wait gave up";
     case TL_ERR_DEVICE_RANGE: return "TL_ERR_DEVICE_RANGE: a per-lane device value was out of range";
+    case TL_ERR_DEVICE_CAPACITY: return "TL_ERR_DEVICE_CAPACITY: too few free pages";
   }
   return "unknown tl_status";
 }
@@ -485,6 +486,7 @@ tl_status tl_storeh_poll_status(void* workspace, size_t workspace_bytes, tl_stre
   }
   if (word & tl::kStatusTimeout) return fail(TL_ERR_DEVICE_TIMEOUT, "device status word 0x%x", word);
   if (word & tl::kStatusRange) return fail(TL_ERR_DEVICE_RANGE, "device status word 0x%x", word);
+  if (word & tl::kStatusFull) return fail(TL_ERR_DEVICE_CAPACITY, "device status word 0x%x", word);
   return TL_OK;
 }
 

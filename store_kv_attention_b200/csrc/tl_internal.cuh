@@ -15,6 +15,7 @@ namespace tl {
 enum : uint32_t {
   kStatusRange = 1u << 0,    // a lane's loops / ctx_len was out of range; the lane was skipped
   kStatusTimeout = 1u << 1,  // a bounded wait gave up
+  kStatusFull = 1u << 2,     // a paged cache had too few free pages
 };
 
 constexpr int kInt4Group = 64;

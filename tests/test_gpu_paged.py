@@ -1,0 +1,542 @@
+"""The paged K/V cache on the GPU, through the binding: append, decode and prompt attention against the FP64
+oracle, the operations on pages against the oracle's list walks, and all of them together.
+
+Tolerance of the attention, element by element (u = half a step of the 16-bit type, 2^-11 or 2^-8):
+    |got - want| <= u |want| + A (u + e),   A = sum_c p_c |v_c|
+the output's rounding, and the rounding of every weight p_c to 16 bits.  e bounds the relative error of
+a weight and of the sum: exp2 (2^-21 for the two), the FP32 sums (n 2^-24), and an error of the score,
+2^-23 hd scale max_c sum_d |q_d k_cd|, in exponent and maximum, so twice.  FP16 values below 2^-14 are
+spaced 2^-24: 2^-25 more for the output, and n 2^-25 max |v| for the weights (the largest is at least 1).
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged_oracle
+
+pytestmark = pytest.mark.gpu
+
+FP16, BF16 = torch.float16, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def tl():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from store_kv_attention_b200 import build_lib
+    build_lib.build()
+    import store_kv_attention_b200 as m
+    return m
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _check(got, res, dtype, hd, scale, n, vmax=None):
+    want, mag, reach = res
+    got = _np(got) if isinstance(got, torch.Tensor) else got
+    u = 2.0 ** -11 if dtype == FP16 else 2.0 ** -8
+    e = 2.0 ** -21 + n * 2.0 ** -24 + 2 * 2.0 ** -23 * hd * scale * np.nan_to_num(reach)[..., None]
+    tol = u * np.abs(want) + mag * (u + e) * 1.01
+    if dtype == FP16:
+        tol = tol + 2.0 ** -25 * (1 + n * vmax)
+    assert np.isfinite(got).all()
+    worst = (np.abs(got - want) / np.maximum(tol, 1e-30)).max()
+    assert worst <= 1.0, f"{worst:.3g} of the tolerance"
+
+
+class Rig:
+    """A cache whose sequences hold random K and V in pages of a random order; everything else is NaN."""
+
+    def __init__(self, tl, lens, *, kv, group, hd, page, dtype, layers=2, seed=0, spare=0, seqs=None, n_lanes=None, split=0):
+        self.tl, self.hd, self.dtype, self.kv, self.heads, self.page = tl, hd, dtype, kv, kv * group, page
+        rng = np.random.default_rng(seed)
+        need = [-(-n // page) for n in lens]
+        max_pages = max(1, max(need)) + spare
+        n_pages = sum(need) + 3
+        n_seqs = len(lens) if seqs is None else max(seqs) + 2
+        desc = tl.PagedDesc(layers, n_pages, page, kv, hd, n_seqs, max_pages, tl.TL_KV_FP16 if dtype == FP16 else tl.TL_KV_BF16)
+        self.cache = tl.PagedCache(desc, self.heads, n_lanes or len(lens), split_rows=split)
+        self.cache.k.fill_(float("nan"))
+        self.cache.v.fill_(float("nan"))
+        order = rng.permutation(n_pages).astype(np.int32)
+        self.seqs = list(range(len(lens))) if seqs is None else seqs
+        table = np.full((n_seqs, max_pages), -1, np.int32)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        at = 0
+        for b, n in enumerate(lens):
+            table[self.seqs[b], :need[b]] = order[at:at + need[b]]
+            for j in range(need[b]):
+                m = min(page, n - j * page)
+                for pool in (self.cache.k, self.cache.v):
+                    pool[:, int(order[at + j]), :, :m] = torch.randn((layers, kv, m, hd), generator=g, device="cuda").to(dtype)
+            at += need[b]
+        self.table = table
+        self.cache.table.copy_(torch.from_numpy(table))
+        self.cache.refs[torch.from_numpy(order[:at].astype(np.int64)).cuda()] = 1
+        self.lens, self.g = list(lens), g
+
+    def queries(self, n, sharp=1.0):
+        return (torch.randn((n, self.heads, self.hd), generator=self.g, device="cuda") * sharp).to(self.dtype)
+
+    def pools(self, layer):
+        return _np(self.cache.k[layer]), _np(self.cache.v[layer])
+
+    def vmax(self, layer):
+        return float(np.nanmax(np.abs(self.pools(layer)[1])))
+
+    def check_decode(self, layer, q, out, lens=None, scale=None):
+        lens = self.lens if lens is None else lens
+        scale = scale or self.hd ** -0.5
+        res = paged_oracle.decode(*self.pools(layer), self.table, _np(q), lens, self.seqs, scale)
+        _check(out, res, self.dtype, self.hd, scale, max(max(lens), 1), self.vmax(layer))
+
+    def check_prompt(self, layer, q, cu, out, kv=None, scale=None):
+        kv = self.lens if kv is None else kv
+        scale = scale or self.hd ** -0.5
+        res = paged_oracle.prompt(*self.pools(layer), self.table, _np(q), cu, kv, self.seqs, scale)
+        inside = ~np.isnan(res[0]).any(axis=(1, 2))
+        got = _np(out)
+        assert np.isnan(got[~inside]).all(), "rows outside every lane were written"
+        _check(got[inside], [r[inside] for r in res], self.dtype, self.hd, scale, max(max(kv), 1), self.vmax(layer))
+
+    def ok(self):
+        assert self.tl.poll_status(self.cache) == self.tl.TL_OK
+
+
+# ---------------------------------------------------------------------------------------- append
+@pytest.mark.parametrize("kv,hd,page,dtype", [(8, 128, 16, BF16), (1, 64, 128, FP16), (3, 128, 32, FP16), (16, 64, 64, BF16)])
+def test_append_writes_rows_where_the_table_says(tl, kv, hd, page, dtype):
+    lens = [40, 0, 129, 7, 300]
+    rig = Rig(tl, [n + 20 for n in lens], kv=kv, group=1, hd=hd, page=page, dtype=dtype)
+    start = [3, 0, 17, 20, 0]
+    cu = np.cumsum([2] + lens)            # the first two rows and the last three belong to nobody
+    rows = int(cu[-1]) + 3
+    wide = torch.randn((rows, 3, kv, hd), generator=rig.g, device="cuda").to(dtype)   # K and V inside a wider row
+    k, v = wide[:, 1], wide[:, 2]
+    want = [rig.cache.k.clone(), rig.cache.v.clone()]
+    for b, n in enumerate(lens):
+        for i in range(n):
+            pos = start[b] + i
+            for pool, x in zip(want, (k, v)):
+                pool[1, rig.table[b, pos // page], :, pos % page] = x[cu[b] + i]
+    tl.paged_append(rig.cache, 1, k, v, _i32(start), cu_rows=_i32(cu.tolist()))
+    rig.ok()
+    for a, b in zip((rig.cache.k, rig.cache.v), want):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def test_append_skips_what_it_may_not_write(tl):
+    """Out of range, no page, a shared page: not written and reported; the other lanes' rows are."""
+    rig = Rig(tl, [20, 20, 20, 20, 20, 20], kv=2, group=1, hd=64, page=16, dtype=FP16)
+    rig.cache.refs[int(rig.table[3, 1])] = 2
+    rig.cache.table[4, 1] = -1
+    x = torch.randn((6, 2, 64), generator=rig.g, device="cuda").to(FP16)
+    want = rig.cache.k.clone()
+    want[0, rig.table[0, 1], :, 1] = x[0]
+    want[0, rig.table[5, 0], :, 4] = x[5]
+    tl.paged_append(rig.cache, 0, x, x, _i32([17, -1, 32, 17, 17, 4]), seqs=_i32([0, 1, 2, 3, 4, 5]))
+    assert tl.poll_status(rig.cache) == tl.TL_ERR_DEVICE_RANGE
+    assert torch.equal(rig.cache.k.view(torch.int16), want.view(torch.int16))
+    tl.paged_append(rig.cache, 0, x[:2], x[:2], _i32([0, 0]), seqs=_i32([6, -1]))
+    assert tl.poll_status(rig.cache) == tl.TL_ERR_DEVICE_RANGE
+    assert torch.equal(rig.cache.k.view(torch.int16), want.view(torch.int16))
+
+
+# ---------------------------------------------------------------------------------------- decode
+@pytest.mark.parametrize("kv,group,hd,page,dtype,lens,split", [
+    (4, 1, 128, 16, FP16, [0, 1, 15, 16, 17, 63, 64, 65], 0),
+    (2, 4, 64, 32, BF16, [127, 128, 129, 1000, 2], 0),
+    (1, 8, 128, 64, BF16, [5000], 0),
+    (2, 5, 128, 128, FP16, [300, 1, 2049], 128),
+    (1, 20, 64, 16, FP16, [513, 40], 256),       # two tiles of query heads, the second one partly filled
+    (3, 16, 128, 16, BF16, [4097, 31], 0),
+    (16, 1, 64, 16, FP16, [2049], 0),
+])
+def test_decode_matches_oracle(tl, kv, group, hd, page, dtype, lens, split):
+    rig = Rig(tl, lens, kv=kv, group=group, hd=hd, page=page, dtype=dtype, split=split)
+    q = rig.queries(len(lens))
+    out = torch.full_like(q, float("nan"))
+    tl.paged_attn_decode(rig.cache, 1, q, _i32(lens), out)
+    rig.ok()
+    rig.check_decode(1, q, out)
+
+
+def test_decode_sharp_scores_scale_and_strided_queries(tl):
+    """Large scores (one weight near 1), a scale of the caller's, queries inside wider rows, chosen sequences."""
+    lens = [700, 64, 33]
+    rig = Rig(tl, lens, kv=2, group=4, hd=128, page=32, dtype=BF16, seqs=[4, 0, 2])
+    wide = rig.queries(6, sharp=6.0).view(3, 2, 8, 128)
+    q, out = wide[:, 1], torch.full((3, 8, 128), float("nan"), dtype=BF16, device="cuda")
+    tl.paged_attn_decode(rig.cache, 0, q, _i32(lens), out, seqs=_i32(rig.seqs), scale=0.31)
+    rig.ok()
+    rig.check_decode(0, q, out, scale=float(np.float32(0.31)))
+
+
+def test_decode_lanes_do_not_depend_on_each_other(tl):
+    """With a split length given, a lane's bits are those of its solo run, whatever lies beside it."""
+    lens = [900, 3, 4000, 257]
+    rig = Rig(tl, lens, kv=2, group=2, hd=128, page=16, dtype=FP16, split=256)
+    q = rig.queries(4)
+    out, solo = torch.empty_like(q), torch.empty_like(q)
+    tl.paged_attn_decode(rig.cache, 0, q, _i32(lens), out)
+    for b in range(4):
+        tl.paged_attn_decode(rig.cache, 0, q[b:b + 1], _i32(lens[b:b + 1]), solo[b:b + 1], seqs=_i32([b]))
+    rig.ok()
+    assert torch.equal(out, solo)
+
+
+def test_decode_skips_and_reports(tl):
+    """Lanes out of range are not written; positions without a page are left out."""
+    lens = [40, 40, 40, 40]
+    rig = Rig(tl, lens, kv=1, group=2, hd=64, page=16, dtype=FP16, spare=1)
+    rig.cache.table[3, 1] = rig.cache.desc.n_pages
+    q = rig.queries(4)
+    out = torch.full_like(q, float("nan"))
+    tl.paged_attn_decode(rig.cache, 0, q, _i32([40, -1, 65, 40]), out)
+    assert tl.poll_status(rig.cache) == tl.TL_ERR_DEVICE_RANGE
+    assert torch.isnan(out[1:3]).all()
+    k, v = rig.pools(0)
+    for b, keep in ((0, np.arange(40)), (3, np.r_[0:16, 32:40])):
+        for h in range(2):
+            kk, vv = (np.concatenate([p[pg, 0] for pg in np.maximum(rig.table[b, :3], 0)])[keep] for p in (k, v))
+            res = paged_oracle.attend(_np(q[b, h])[None], kk, vv, 0.125)
+            _check(_np(out[b, h])[None], res, FP16, 64, 0.125, 40, rig.vmax(0))
+    tl.paged_attn_decode(rig.cache, 0, q[:2], _i32([40, 40]), out[:2], seqs=_i32([4, -1]))
+    assert tl.poll_status(rig.cache) == tl.TL_ERR_DEVICE_RANGE
+
+
+def test_decode_offsets_past_32_bits(tl):
+    """Pages whose elements lie past 2^32 bytes and 2^31 elements into the pool."""
+    page, kv, hd, n_pages = 128, 16, 128, 9000           # 2.36e9 elements a layer
+    desc = tl.PagedDesc(1, n_pages, page, kv, hd, 2, 4, tl.TL_KV_FP16)
+    k = torch.zeros((1, n_pages, kv, page, hd), dtype=FP16, device="cuda")
+    v = torch.zeros_like(k)
+    cache = tl.PagedCache(desc, kv, 2, k=k, v=v)
+    far = [n_pages - 1, 8300]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rows = torch.randn((200, kv, hd), generator=g, device="cuda").to(FP16)
+    cache.table[1, :2] = _i32(far)
+    tl.paged_append(cache, 0, rows, rows, _i32([0]), cu_rows=_i32([0, 200]), seqs=_i32([1]))
+    q = torch.randn((200, kv, hd), generator=g, device="cuda").to(FP16)
+    out, tok = torch.empty_like(q), torch.empty_like(q[:1])
+    tl.paged_prompt_attn(cache, 0, q, _i32([0, 200]), _i32([200]), out, seqs=_i32([1]))
+    tl.paged_attn_decode(cache, 0, q[199:], _i32([200]), tok, seqs=_i32([1]))
+    cache.refs[far[1]] = 1
+    tl.paged_copy(cache, _i32([far[1]]), _i32([far[0]]))
+    assert tl.poll_status(cache) == tl.TL_OK
+    assert torch.equal(k[0, far[0], :, :72], rows[128:].transpose(0, 1)) and torch.equal(k[0, far[0]], k[0, far[1]])
+    x = _np(rows)
+    for h in (0, kv - 1):
+        res = paged_oracle.attend(_np(q[:, h]), x[:, h], x[:, h], hd ** -0.5, np.arange(200))
+        _check(_np(out[:, h]), res, FP16, hd, hd ** -0.5, 200, np.abs(x).max())
+        _check(_np(tok[:, h]), [r[199:] for r in res], FP16, hd, hd ** -0.5, 200, np.abs(x).max())
+
+
+# ---------------------------------------------------------------------------------------- prompts
+@pytest.mark.parametrize("kv,group,hd,page,dtype,lens,cached", [
+    (2, 1, 64, 16, FP16, [1], [0]),
+    (1, 4, 128, 16, FP16, [130, 1, 0, 257, 64], [0, 0, 5, 0, 0]),
+    (2, 2, 128, 128, BF16, [300, 128], [0, 0]),
+    (2, 3, 64, 32, BF16, [200, 33], [0, 100]),
+    (1, 12, 128, 64, FP16, [70, 5], [600, 127]),          # four heads of each twelve packed
+    (1, 1, 128, 16, BF16, [513], [0]),
+    (2, 8, 64, 16, FP16, [40, 41, 39], [1000, 0, 88]),
+    (1, 128, 64, 16, BF16, [3, 2], [0, 50]),              # one token a tile
+])
+def test_prompt_matches_oracle(tl, kv, group, hd, page, dtype, lens, cached):
+    total = [a + b for a, b in zip(lens, cached)]
+    rig = Rig(tl, total, kv=kv, group=group, hd=hd, page=page, dtype=dtype)
+    cu = np.cumsum([1] + lens).tolist()                    # a row before and two behind that belong to nobody
+    q = rig.queries(cu[-1] + 2)
+    out = torch.full_like(q, float("nan"))
+    tl.paged_prompt_attn(rig.cache, 1, q, _i32(cu), _i32(total), out)
+    rig.ok()
+    rig.check_prompt(1, q, cu, out)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_prompt_growing_maxima_and_strided_queries(tl, hd):
+    """Keys that grow along the sequence, so that every tile raises the maxima by far more than the rescale's
+    threshold; scores up to about 60; a scale of the caller's; queries inside wider rows."""
+    n = 600
+    rig = Rig(tl, [n], kv=1, group=2, hd=hd, page=64, dtype=BF16, layers=1)
+    ramp = torch.linspace(0.1, 6.0, 640, device="cuda").view(10, 64)
+    for j in range(10):
+        rig.cache.k[0, int(rig.table[0, j])] *= ramp[j].view(1, 64, 1).to(BF16)
+    wide = rig.queries(3 * n).view(n, 3, 2, hd)
+    q = wide[:, 2]
+    out = torch.full((n, 2, hd), float("nan"), dtype=BF16, device="cuda")
+    tl.paged_prompt_attn(rig.cache, 0, q, _i32([0, n]), _i32([n]), out, scale=0.25)
+    rig.ok()
+    rig.check_prompt(0, q, [0, n], out, scale=0.25)
+
+
+def test_prompt_rows_that_attend_nothing(tl):
+    """Queries at negative positions give zeros, a lane without cached positions too."""
+    rig = Rig(tl, [20, 0], kv=1, group=2, hd=64, page=16, dtype=FP16)
+    cu = [0, 150, 153]
+    q = rig.queries(153)
+    out = torch.full_like(q, float("nan"))
+    tl.paged_prompt_attn(rig.cache, 0, q, _i32(cu), _i32([20, 0]), out)
+    rig.ok()
+    assert not out[:130].any() and not out[150:].any()
+    rig.check_prompt(0, q, cu, out)
+
+
+@pytest.mark.parametrize("hd,page,dtype", [(128, 16, BF16), (64, 128, FP16)])
+def test_prompt_is_causal_whatever_later_positions_hold(tl, hd, page, dtype):
+    """NaN and infinities in K and V of later positions reach only the queries that attend them."""
+    n, at = 390, 301
+    rig = Rig(tl, [n], kv=1, group=2, hd=hd, page=page, dtype=dtype, layers=1)
+    q = rig.queries(n)
+    out, clean = torch.empty_like(q), torch.empty_like(q)
+    tl.paged_prompt_attn(rig.cache, 0, q, _i32([0, n]), _i32([n]), clean)
+    slot = lambda pos: (0, int(rig.table[0, pos // page]), 0, pos % page)  # noqa: E731
+    rig.cache.v[slot(at)][3] = float("inf")
+    rig.cache.v[slot(at + 20)][5] = float("nan")
+    tl.paged_prompt_attn(rig.cache, 0, q, _i32([0, n]), _i32([n]), out)
+    rig.ok()
+    assert torch.equal(out[:at], clean[:at])
+    assert torch.isinf(out[at:, :, 3]).all() and (out[at:, :, 3] > 0).all()
+    assert torch.isnan(out[at + 20:, :, 5]).all() and torch.equal(out[:at + 20, :, 5], clean[:at + 20, :, 5])
+    rest = [d for d in range(hd) if d not in (3, 5)]
+    assert torch.equal(out[..., rest], clean[..., rest])
+    rig.cache.k[slot(at)] = float("nan")
+    tl.paged_prompt_attn(rig.cache, 0, q, _i32([0, n]), _i32([n]), out)
+    assert torch.equal(out[:at], clean[:at]) and torch.isnan(out[at:]).all()
+
+
+def test_prompt_skips_and_reports(tl):
+    rig = Rig(tl, [40, 40, 40, 40], kv=1, group=1, hd=64, page=16, dtype=FP16)
+    rig.cache.table[1, 2] = -1
+    q = rig.queries(160)
+    cu = [0, 40, 80, 120, 160]
+    for lens, seqs, lanes in (([40, 40, 49, 40], [0, 1, 2, 3], (1, 2)), ([40, 40, -1, 40], [0, 4, 2, -1], (1, 2, 3))):
+        out = torch.full_like(q, float("nan"))
+        tl.paged_prompt_attn(rig.cache, 0, q, _i32(cu), _i32(lens), out, seqs=_i32(seqs))
+        assert tl.poll_status(rig.cache) == tl.TL_ERR_DEVICE_RANGE
+        for b in range(4):
+            assert torch.isnan(out[cu[b]:cu[b + 1]]).all() == (b in lanes)
+    for bad in ([0, 40, 30, 120, 161], [-1, 40, 80, 120, 160]):
+        out = torch.full_like(q, float("nan"))
+        tl.paged_prompt_attn(rig.cache, 0, q, _i32(bad), _i32([30, 30, 30, 30]), out, seqs=_i32([0, 0, 2, 3]))
+        assert tl.poll_status(rig.cache) == tl.TL_ERR_DEVICE_RANGE
+
+
+def test_prompt_row_equals_decode_of_the_same_position(tl):
+    """The last row of a prompt and the decode of its token agree within the roundings of both."""
+    lens = [500, 77]
+    rig = Rig(tl, lens, kv=2, group=4, hd=128, page=32, dtype=FP16)
+    q = rig.queries(577)
+    out, tok = torch.empty_like(q), torch.empty_like(q[:2])
+    tl.paged_prompt_attn(rig.cache, 0, q, _i32([0, 500, 577]), _i32(lens), out)
+    tl.paged_attn_decode(rig.cache, 0, q[[499, 576]], _i32(lens), tok)
+    rig.check_decode(0, q[[499, 576]], tok)
+    rig.check_decode(0, q[[499, 576]], out[[499, 576]])
+
+
+# ---------------------------------------------------------------------------------------- pages
+class Twin:
+    """A cache beside the oracle's list walks: each operation on both, then everything compared."""
+
+    def __init__(self, tl, n_pages, page, max_seqs, max_pages, layers=3, kv=2, hd=64):
+        self.tl = tl
+        self.o = paged_oracle.Pages(n_pages, page, max_seqs, max_pages)
+        self.cache = tl.PagedCache(tl.PagedDesc(layers, n_pages, page, kv, hd, max_seqs, max_pages), kv, min(max_seqs, 1024))
+        n = self.cache.k.numel()
+        self.cache.k.view(torch.int16).copy_(torch.arange(n, device="cuda").view(self.cache.k.shape))
+        self.cache.v.view(torch.int16).copy_((torch.arange(n, device="cuda") * 7 + 1).view(self.cache.k.shape))
+        self.k, self.v = self.cache.k.clone(), self.cache.v.clone()
+
+    def do(self, op, *lists):
+        self.o.flags = set()
+        moves = getattr(self.o, op)(*lists)
+        getattr(self.tl, "paged_" + op)(self.cache, *[None if x is None else _i32(x) for x in lists])
+        for pool in (self.k, self.v):
+            was = pool.clone()
+            for a, b in moves:
+                pool[:, b] = was[:, a]
+        want = self.tl.TL_ERR_DEVICE_RANGE if "range" in self.o.flags else \
+            self.tl.TL_ERR_DEVICE_CAPACITY if "full" in self.o.flags else self.tl.TL_OK
+        assert self.tl.poll_status(self.cache) == want, op
+        assert np.array_equal(self.cache.table.cpu().numpy(), self.o.table), op
+        assert np.array_equal(self.cache.refs.cpu().numpy(), self.o.refs), op
+        assert torch.equal(self.cache.k.view(torch.int16), self.k.view(torch.int16)), op
+        assert torch.equal(self.cache.v.view(torch.int16), self.v.view(torch.int16)), op
+
+
+def test_pages_of_a_serving_loop(tl):
+    t = Twin(tl, n_pages=70, page=16, max_seqs=12, max_pages=9)
+    t.do("reserve", [3, 0, 7], [0, 0, 0], [100, 16, 33])
+    t.do("fork", [3, 3, 0], [4, 5, 9], [100, 64, 16])
+    t.do("reserve", [4, 3, 5, 9], [100, 100, 64, 16], [1, 1, 1, 20])   # all sharers of a last page copy it
+    t.do("free", [3], [30])
+    t.do("free", [7, 4, 7], None)                                      # one listed twice
+    t.do("reserve", [7, 11], [0, 0], [1, 144])
+    t.do("compact")
+    t.do("copy", [0, 5, 1], [60, 61, 62])
+    t.do("free", [3, 5, 9], [17, 0, 16])
+    t.do("compact")
+    t.do("compact")
+    t.do("free", list(range(12)), None)
+    t.do("compact")
+    assert not t.o.refs.any()
+
+
+def test_pages_refusals(tl):
+    t = Twin(tl, n_pages=24, page=32, max_seqs=6, max_pages=4)
+    t.do("reserve", [0, 1, 0, 6, -1, 2, 3], [0, 0, 0, 0, 0, -1, 100], [64, 1, 5, 1, 1, 1, 40])  # listed twice, out of range, too long
+    t.do("reserve", [3], [7], [2 ** 31 - 8])
+    t.do("fork", [0, 0, 1, 2, 9, 0, 4], [2, 2, 0, 3, 4, 5, 5], [64, 1, 1, 1, 1, 65, 0])         # dst twice, src a dst, lacking pages
+    t.do("free", [6, 2, -3, 0], [0, -1, 0, 31])
+    t.do("copy", [0, 1, 2, 24, 3, -1, 8], [10, 11, 10, 12, 0, 13, 8])
+    t.do("reserve", [0, 3, 4, 5], [0, 0, 0, 0], [0, 128, 128, 128])
+    t.do("reserve", [1, 2, 4], [0, 0, 0], [128, 128, 128])                                      # the last is not covered
+    t.do("reserve", [4, 1], [0, 0], [128, 1])
+
+
+@pytest.mark.parametrize("n_pages,max_pages", [(20001, 400), (40000, 3000)])
+def test_pages_at_size(tl, n_pages, max_pages):
+    """Several scan rounds over the pool and over the candidates of one call, odd sizes, random lists."""
+    rng = np.random.default_rng(n_pages)
+    t = Twin(tl, n_pages=n_pages, page=16, max_seqs=200, max_pages=max_pages, layers=1, kv=1)
+    hi = max_pages * 16
+    lens = [0] * 200
+    for i in range(90):
+        lens[i] = int(min(rng.integers(1, hi), n_pages * 16 // 120))
+    lens[50] = hi                                   # one long prompt beside the others
+    t.do("reserve", list(range(90)), [0] * 90, lens[:90])
+    t.do("free", [int(i) for i in rng.permutation(90)[:45]], None)
+    src = [i for i in range(90) if (t.o.table[i] >= 0).any()][:40]
+    t.do("fork", src, list(range(100, 100 + len(src))), [min(lens[i], int(rng.integers(0, hi))) for i in src])
+    t.do("compact")
+    t.do("reserve", list(range(100, 100 + len(src))), [int(rng.integers(0, lens[i])) for i in src], [3] * len(src))
+    t.do("compact")
+
+
+def test_reserve_a_thousand_sequences(tl):
+    t = Twin(tl, n_pages=1500, page=16, max_seqs=1030, max_pages=2, layers=1, kv=1)
+    order = np.random.default_rng(0).permutation(1030)[:1024].tolist()
+    t.do("reserve", order, [0] * 1024, [1 + i % 16 for i in range(1024)])
+    t.do("reserve", order, [16] * 1024, [1] * 1024)          # 476 of them are covered
+    t.do("free", order, [16] * 1024)
+    t.do("compact")
+
+
+# ---------------------------------------------------------------------------------------- together
+def _serve(tl, cache, layers, x, out):
+    """Prompts into the cache, forks, three tokens each, a rejected token taken back, compaction, one more token."""
+    kv, heads = cache.desc.n_kv_heads, cache.n_heads
+    n_prompt = [50, 7, 130]
+    cu = _i32([0, 50, 57, 187])
+    seqs, zero = _i32([0, 1, 2]), _i32([0, 0, 0])
+    tl.paged_reserve(cache, seqs, zero, _i32(n_prompt))
+    for la in range(layers):
+        q, k, v = x[la, :187, :heads], x[la, :187, heads:heads + kv], x[la, :187, heads + kv:]
+        tl.paged_append(cache, la, k, v, zero, cu_rows=cu, seqs=seqs)
+        tl.paged_prompt_attn(cache, la, q, cu, _i32(n_prompt), out[la, :187], seqs=seqs)
+    tl.paged_fork(cache, _i32([0, 2]), _i32([3, 4]), _i32([50, 130]))
+    lanes, at = _i32([0, 1, 2, 3, 4]), 187
+    lens = [50, 7, 130, 50, 130]
+    for step in range(4):
+        if step == 3:                                  # the last token is taken back, then the pool compacted
+            lens = [n - 1 for n in lens]
+            tl.paged_free(cache, lanes, _i32(lens))
+            tl.paged_compact(cache)
+        tl.paged_reserve(cache, lanes, _i32(lens), _i32([1] * 5))
+        for la in range(layers):
+            row = x[la, at:at + 5]
+            tl.paged_append(cache, la, row[:, heads:heads + kv], row[:, heads + kv:], _i32(lens), seqs=lanes)
+            tl.paged_attn_decode(cache, la, row[:, :heads], _i32([n + 1 for n in lens]), out[la, at:at + 5], seqs=lanes)
+        lens = [n + 1 for n in lens]
+        at += 5
+    return lens
+
+
+@pytest.mark.parametrize("dtype,page", [(FP16, 16), (BF16, 64)])
+def test_serving_run_matches_plain_attention(tl, dtype, page):
+    """The operators as they are used together, against attention over plainly kept K and V."""
+    layers, kv, heads, hd = 2, 2, 6, 64
+    cache = tl.PagedCache(tl.PagedDesc(layers, 60, page, kv, hd, 6, 12, tl.TL_KV_FP16 if dtype == FP16 else tl.TL_KV_BF16), heads, 5)
+    cache.k.fill_(float("nan"))
+    cache.v.fill_(float("nan"))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn((layers, 207, heads + 2 * kv, hd), generator=g, device="cuda").to(dtype)
+    out = torch.empty((layers, 207, heads, hd), dtype=dtype, device="cuda")
+    _serve(tl, cache, layers, x, out)
+    assert tl.poll_status(cache) == tl.TL_OK
+    # rows of each sequence at each step, as indices into x
+    hist = [list(range(0, 50)), list(range(50, 57)), list(range(57, 187))]
+    hist += [hist[0], hist[2]]
+    want = [(b, i, hist[b][: i + 1], hist[b][i]) for b in range(3) for i in range(len(hist[b]))]
+    at = 187
+    for step in range(4):
+        if step == 3:
+            hist = [h[:-1] for h in hist]
+        hist = [h + [at + b] for b, h in enumerate(hist)]
+        want += [(b, len(h) - 1, h, h[-1]) for b, h in enumerate(hist)]
+        at += 5
+    xs, got = _np(x), _np(out)
+    vmax = np.abs(xs).max()
+    for la in range(layers):
+        for b, i, rows, r in want[::7] + want[-20:]:
+            for h in range(heads):
+                kk, vv = xs[la, rows, heads + h // 3], xs[la, rows, heads + kv + h // 3]
+                res = paged_oracle.attend(xs[la, r, h][None], kk, vv, hd ** -0.5)
+                _check(got[la, r, h][None], res, dtype, hd, hd ** -0.5, len(rows), vmax)
+
+
+def test_graph_replay_on_a_side_stream_equals_eager(tl):
+    """The calls captured, replayed twice from the same start, on another stream: the bits of the eager run.  Two
+    graphs share the workspace, replayed one after the other."""
+    rig = Rig(tl, [0, 40, 700, 129], kv=2, group=4, hd=128, page=16, dtype=BF16, spare=2)
+    lens, one = _i32([0, 40, 700, 129]), _i32([1] * 4)
+    after = _i32([1, 41, 701, 130])
+    seqs = _i32([0, 1, 2, 3])
+    rows = torch.randn((4, 12, 128), generator=rig.g, device="cuda").to(BF16)
+    start = [t.clone() for t in (rig.cache.k, rig.cache.v, rig.cache.table, rig.cache.refs)]
+    cu = _i32([0, 1, 2, 3, 4])
+    out, pr = torch.empty_like(rows[:, :8]), torch.empty_like(rows[:, :8])
+
+    def step():
+        tl.paged_reserve(rig.cache, seqs, lens, one)
+        tl.paged_append(rig.cache, 1, rows[:, 8:10], rows[:, 10:], lens)
+        tl.paged_attn_decode(rig.cache, 1, rows[:, :8], after, out)
+
+    def step2():
+        tl.paged_prompt_attn(rig.cache, 1, rows[:, :8], cu, after, pr)
+        tl.paged_attn_decode(rig.cache, 0, rows[:, :8], lens, out2)
+    out2 = torch.empty_like(out)
+
+    def reset():
+        for a, b in zip((rig.cache.k, rig.cache.v, rig.cache.table, rig.cache.refs), start):
+            a.copy_(b)
+        for o in (out, pr, out2):
+            o.fill_(float("nan"))
+    step()
+    step2()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (out, pr, out2, rig.cache.table, rig.cache.refs, rig.cache.k.view(torch.int16))]
+    side = torch.cuda.Stream()
+    reset()
+    torch.cuda.synchronize()
+    graphs = []
+    with torch.cuda.stream(side):
+        for f in (step, step2):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                f()
+            graphs.append(g)
+        for _ in range(2):
+            reset()
+            for g in graphs:
+                g.replay()
+    side.synchronize()
+    rig.ok()
+    for a, b in zip((out, pr, out2, rig.cache.table, rig.cache.refs, rig.cache.k.view(torch.int16)), want):
+        assert torch.equal(a.view(torch.int16) if a.is_floating_point() else a, b.view(torch.int16) if b.is_floating_point() else b)
