@@ -510,56 +510,63 @@ def paged_workspace_bytes(desc: PagedDesc, n_heads: int, n_lanes: int, split_row
 class PagedCache:
     """Device buffers of one paged cache: k, v [n_layers, n_pages, n_kv_heads, page_size, head_dim],
     table int32 [max_seqs, max_pages] (-1), refs int32 [n_pages] (0) and a zeroed workspace for calls
-    of up to n_lanes lanes of n_heads query heads.  Buffers of the caller's own can be given instead."""
+    of up to n_lanes lanes of n_heads query heads.  Buffers of the caller's own can be given instead.
+    A cache keeps its buffers for good: what the library is told of them is set down here once."""
 
     def __init__(self, desc: PagedDesc, n_heads: int, n_lanes: int, device="cuda", split_rows: int = 0, k=None, v=None,
                  table=None, refs=None):
         import torch
-        self.desc, self.n_heads, self.split_rows = desc, n_heads, split_rows
+        self.desc, self.n_heads, self.split_rows = dataclasses.replace(desc), n_heads, split_rows
         self.ws_bytes = paged_workspace_bytes(desc, n_heads, n_lanes, split_rows)
         self.dtype = torch.float16 if desc.dtype == TL_KV_FP16 else torch.bfloat16
         pool = (desc.n_layers, desc.n_pages, desc.n_kv_heads, desc.page_size, desc.head_dim)
         rows = (desc.max_seqs, desc.max_pages)
         if k is not None:
             device = k.device
-        self.k = torch.empty(pool, dtype=self.dtype, device=device) if k is None else k
-        self.v = torch.empty(pool, dtype=self.dtype, device=device) if v is None else v
-        self.table = torch.full(rows, -1, dtype=torch.int32, device=device) if table is None else table
-        self.refs = torch.zeros(desc.n_pages, dtype=torch.int32, device=device) if refs is None else refs
-        self.device = self.k.device
-        for name, t, shape, dt in (("k", self.k, pool, self.dtype), ("v", self.v, pool, self.dtype),
-                                   ("table", self.table, rows, torch.int32), ("refs", self.refs, (desc.n_pages,), torch.int32)):
+        k = torch.empty(pool, dtype=self.dtype, device=device) if k is None else k
+        v = torch.empty(pool, dtype=self.dtype, device=device) if v is None else v
+        table = torch.full(rows, -1, dtype=torch.int32, device=device) if table is None else table
+        refs = torch.zeros(desc.n_pages, dtype=torch.int32, device=device) if refs is None else refs
+        self.device, self._index = k.device, k.get_device()
+        for name, t, shape, dt in (("k", k, pool, self.dtype), ("v", v, pool, self.dtype),
+                                   ("table", table, rows, torch.int32), ("refs", refs, (desc.n_pages,), torch.int32)):
             _paged_tensor(self, name, t, dt, shape)
         self.workspace = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        self._buffers = (k, v, table, refs)
+        self._desc_c = desc.c()
+        self._head = (ctypes.byref(self._desc_c), self.c())
+        self._tail = (self.workspace.data_ptr(), self.ws_bytes)
+
+    k = property(lambda self: self._buffers[0])
+    v = property(lambda self: self._buffers[1])
+    table = property(lambda self: self._buffers[2])
+    refs = property(lambda self: self._buffers[3])
 
     def c(self) -> PagedCacheC:
-        return PagedCacheC(self.k.data_ptr(), self.v.data_ptr(), self.table.data_ptr(), self.refs.data_ptr())
+        return PagedCacheC(*(t.data_ptr() for t in self._buffers))
 
 
-def _paged_tensor(cache: PagedCache, name: str, t, dtype, shape, rows: bool = False):
-    """Raises unless t lies on the cache's device with this type and shape (None: any extent) and is dense
-    (rows: only behind its first axis)."""
+def _paged_tensor(cache: PagedCache, name: str, t, dtype, shape) -> None:
+    """Raises unless t is dense, on the cache's device, with this type and shape."""
+    if t.dtype is dtype and t.get_device() == cache._index and t.shape == shape and t.is_contiguous():
+        return
     if t.device != cache.device:
         raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} is {t.dtype}, not {dtype}")
-    if t.dim() != len(shape) or any(w is not None and w != n for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple('n' if w is None else w for w in shape)}")
-    want = 1
-    for axis in reversed(range(1 if rows else 0, t.dim())):
-        if t.shape[axis] != 1 and t.stride(axis) != want:
-            raise ValueError(f"{name} is not dense: strides {t.stride()}")
-        want *= t.shape[axis]
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    raise ValueError(f"{name} is not dense: strides {t.stride()}")
 
 
-def _paged_rows(cache: PagedCache, name: str, t, heads: int) -> int:
-    """The row stride of [n, heads, head_dim] rows, which may be part of wider rows."""
-    _paged_tensor(cache, name, t, cache.dtype, (None, heads, cache.desc.head_dim), rows=True)
-    if t.shape[0] < 2:
-        return 0
-    if t.stride(0) <= 0:
-        raise ValueError(f"{name} has overlapping rows: strides {t.stride()}")
-    return t.stride(0)
+def _paged_rows(cache: PagedCache, name: str, t, n: int, heads: int) -> int:
+    """The row stride of t [n, heads, head_dim], whose rows may be parts of wider ones (0: dense)."""
+    shape = (n, heads, cache.desc.head_dim)
+    if t.shape == shape and not t.is_contiguous() and t.stride(2) == 1 and t.stride(1) == shape[2] and t.stride(0) > 0:
+        _paged_tensor(cache, name, t[0], cache.dtype, shape[1:])
+        return t.stride(0)
+    _paged_tensor(cache, name, t, cache.dtype, shape)
+    return 0
 
 
 def _paged_ints(cache: PagedCache, n: int, **tensors) -> None:
@@ -570,32 +577,35 @@ def _paged_ints(cache: PagedCache, n: int, **tensors) -> None:
 
 
 def _paged_call(cache: PagedCache, name: str, args, stream) -> None:
-    """Calls name(desc, cache, *args, workspace, its size, stream) with the cache's device current."""
+    """Calls name(desc, cache, *args, workspace, its size, stream) with the cache's device current; the stream
+    None is that device's current one."""
     import torch
-    with torch.cuda.device(cache.device):
-        _check(getattr(_load(), name)(ctypes.byref(cache.desc.c()), cache.c(), *args, cache.workspace.data_ptr(),
-                                      cache.ws_bytes, _stream(stream)), name)
+    if torch.cuda.current_device() != cache._index:
+        with torch.cuda.device(cache._index):
+            return _paged_call(cache, name, args, stream)
+    raw = torch._C._cuda_getCurrentRawStream(cache._index) if stream is None else _stream(stream)
+    st = getattr(_lib_handle or _load(), name)(*cache._head, *args, *cache._tail, raw)
+    if st != TL_OK:
+        _check(st, name)
 
 
 def paged_append(cache: PagedCache, layer: int, k_rows, v_rows, start_pos, cu_rows=None, seqs=None, stream=None) -> None:
     """tl_paged_append: k_rows, v_rows [n, n_kv_heads, head_dim] in the cache's type (rows may be strided);
     start_pos / seqs int32 [n_lanes], cu_rows int32 [n_lanes + 1] (None: one row per lane)."""
-    ks = _paged_rows(cache, "k_rows", k_rows, cache.desc.n_kv_heads)
-    vs = _paged_rows(cache, "v_rows", v_rows, cache.desc.n_kv_heads)
-    if k_rows.shape[0] != v_rows.shape[0]:
-        raise ValueError(f"{k_rows.shape[0]} rows of K, {v_rows.shape[0]} of V")
-    n = int(start_pos.numel())
+    rows, n = k_rows.shape[0], start_pos.numel()
+    ks = _paged_rows(cache, "k_rows", k_rows, rows, cache.desc.n_kv_heads)
+    vs = _paged_rows(cache, "v_rows", v_rows, rows, cache.desc.n_kv_heads)
     _paged_ints(cache, n, start_pos=start_pos, seqs=seqs)
     _paged_ints(cache, n + 1, cu_rows=cu_rows)
-    _paged_call(cache, "tl_paged_append", (layer, _ptr(k_rows), ks, _ptr(v_rows), vs, int(k_rows.shape[0]), _ptr(cu_rows),
+    _paged_call(cache, "tl_paged_append", (layer, _ptr(k_rows), ks, _ptr(v_rows), vs, rows, _ptr(cu_rows),
                                            _ptr(start_pos), _ptr(seqs), n), stream)
 
 
 def paged_attn_decode(cache: PagedCache, layer: int, q, kv_len, out, seqs=None, scale: float = 0.0, stream=None) -> None:
     """tl_paged_attn_decode: q [n_lanes, n_heads, head_dim] (rows may be strided), kv_len / seqs int32 [n_lanes],
     out [n_lanes, n_heads, head_dim]; scale 0: 1 / sqrt(head_dim).  Splits of cache.split_rows positions."""
-    n, heads = int(q.shape[0]), int(q.shape[1])
-    qs = _paged_rows(cache, "q", q, heads)
+    n, heads = q.shape[0], q.shape[1]
+    qs = _paged_rows(cache, "q", q, n, heads)
     _paged_tensor(cache, "out", out, cache.dtype, (n, heads, cache.desc.head_dim))
     _paged_ints(cache, n, kv_len=kv_len, seqs=seqs)
     _paged_call(cache, "tl_paged_attn_decode", (layer, heads, _ptr(q), qs, _ptr(kv_len), _ptr(seqs), float(scale),
@@ -606,8 +616,8 @@ def paged_prompt_attn(cache: PagedCache, layer: int, q, cu_q, kv_len, out, seqs=
                       stream=None) -> None:
     """tl_paged_prompt_attn: packed queries q [n, n_heads, head_dim] (rows may be strided), cu_q int32
     [n_lanes + 1], kv_len / seqs int32 [n_lanes], out [n, n_heads, head_dim]."""
-    n, heads, lanes = int(q.shape[0]), int(q.shape[1]), int(kv_len.numel())
-    qs = _paged_rows(cache, "q", q, heads)
+    n, heads, lanes = q.shape[0], q.shape[1], kv_len.numel()
+    qs = _paged_rows(cache, "q", q, n, heads)
     _paged_tensor(cache, "out", out, cache.dtype, (n, heads, cache.desc.head_dim))
     _paged_ints(cache, lanes, kv_len=kv_len, seqs=seqs)
     _paged_ints(cache, lanes + 1, cu_q=cu_q)
@@ -617,28 +627,28 @@ def paged_prompt_attn(cache: PagedCache, layer: int, q, cu_q, kv_len, out, seqs=
 
 def paged_copy(cache: PagedCache, src, dst, stream=None) -> None:
     """tl_paged_copy: page src[i] to page dst[i] (int32 [n], device), every layer's K and V."""
-    n = int(src.numel())
+    n = src.numel()
     _paged_ints(cache, n, src=src, dst=dst)
     _paged_call(cache, "tl_paged_copy", (_ptr(src), _ptr(dst), n), stream)
 
 
 def paged_fork(cache: PagedCache, src, dst, n_tokens, stream=None) -> None:
     """tl_paged_fork: sequence dst[i] shares the first n_tokens[i] positions of src[i] (int32 [n], device)."""
-    n = int(src.numel())
+    n = src.numel()
     _paged_ints(cache, n, src=src, dst=dst, n_tokens=n_tokens)
     _paged_call(cache, "tl_paged_fork", (_ptr(src), _ptr(dst), _ptr(n_tokens), n), stream)
 
 
 def paged_reserve(cache: PagedCache, seqs, ctx_len, n_new, stream=None) -> None:
     """tl_paged_reserve: pages of its own for positions ctx_len[i] .. + n_new[i] - 1 of sequence seqs[i]."""
-    n = int(seqs.numel())
+    n = seqs.numel()
     _paged_ints(cache, n, seqs=seqs, ctx_len=ctx_len, n_new=n_new)
     _paged_call(cache, "tl_paged_reserve", (_ptr(seqs), _ptr(ctx_len), _ptr(n_new), n), stream)
 
 
 def paged_free(cache: PagedCache, seqs, keep=None, stream=None) -> None:
     """tl_paged_free: the pages behind the first keep[i] positions (None: all) of sequence seqs[i]."""
-    n = int(seqs.numel())
+    n = seqs.numel()
     _paged_ints(cache, n, seqs=seqs, keep=keep)
     _paged_call(cache, "tl_paged_free", (_ptr(seqs), _ptr(keep), n), stream)
 
