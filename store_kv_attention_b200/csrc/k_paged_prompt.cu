@@ -73,7 +73,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, 
       : "memory");
 }
 #define TL_R8(v, o) "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), "=r"(v[o + 6]), "=r"(v[o + 7])
-#define TL_W8(v, o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7])
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
@@ -82,17 +81,31 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      TL_W8(v, 0), TL_W8(v, 8), TL_W8(v, 16), TL_W8(v, 24)
-      : "memory");
-}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Two FP32 values in a 64-bit register, for the packed instructions.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(x));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float a, float b) {
@@ -165,10 +178,11 @@ template <int HD, bool BF16>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     paged_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const PromptParams p) {
-  constexpr int kOperand = PromptSmem<HD>::kOperand, kSlots = PromptSmem<HD>::kSlots;
+  constexpr int kOperand = PromptSmem<HD>::kOperand, kSlots = PromptSmem<HD>::kSlots, kVSlots = kSlots / 2;
   constexpr uint32_t kIdS = idesc16<BF16>(128, 128, false), kIdO = idesc16<BF16>(128, HD, true);
+  static_assert(kSlots % 2 == 0, "V(j) lies in slot 2 (j mod kVSlots) + 1");
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t q_full, full[kSlots], empty[kSlots], s_full[2], p_full[2], o_done[2], near, clean, fin;
+  __shared__ uint64_t q_full, full[kSlots], empty[kSlots], s_full[2], p_most[2], p_full[2], o_done[2], near, clean[kVSlots], fin;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag, dirty;
   __shared__ Job job;
@@ -190,11 +204,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
+      mbar_init(&p_most[t], 128);
       mbar_init(&p_full[t], 128);
       mbar_init(&o_done[t], 1);
     }
     mbar_init(&near, 1);
-    mbar_init(&clean, 64);
+    for (int i = 0; i < kVSlots; ++i) mbar_init(&clean[i], 64);
     mbar_init(&fin, 1);
     abort_flag = 0;
     dirty = 0;
@@ -242,7 +257,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   int loads = 0;                                            // ring loads issued (producer warp)
   bool issued = false;                                      // products issued (warp 8)
 
+  // Registers: 384 x 168 at launch = 256 x 208 + 128 x 88.  A softmax thread holds a row of S.
   if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ------------------------------------------------------------ softmax of tile t, row r
     const int t = warp >> 2, r = threadIdx.x & 127;
     const int tok = tok0 + t * tq + r / p.pack, head = h0 + r % p.pack;
@@ -265,15 +282,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         for (int c = 0; c < 128; ++c)
           if (j * kTile + c > lim) x[c] = -INFINITY;
       }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int c = 0; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      if (__any_sync(0xffffffffu, (top - m) * p.scale2 > kGrow)) {
-        const float to_m = fmaxf(m, top);
-        const float f = m == -INFINITY ? 0.0f : ex2((m - to_m) * p.scale2);
-        m = to_m;
-        l *= f;
+      for (int c = 4; c < 128; ++c) asm("max.NaN.f32 %0, %0, %1;" : "+f"(mx[c & 3]) : "f"(x[c]));
+      float top = mx[0];
+#pragma unroll
+      for (int c = 1; c < 4; ++c) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(mx[c]));
+      const bool grown = !((top - m) * p.scale2 <= kGrow);  // not comparable: a NaN, or nothing attended yet
+      if (__any_sync(0xffffffffu, grown)) {
+        float f = 1.0f;  // a row's result does not depend on the rows beside it
+        if (grown) {
+          const float was = m;
+          asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(top));
+          f = was == -INFINITY ? 0.0f : ex2((was - m) * p.scale2);
+          l *= f;
+        }
         if (j > 0) {
           if (!(good = __all_sync(0xffffffffu, mbar_wait(&o_done[t], (j - 1) & 1, abort_p, kPWait)))) break;
           tc_fence_after();
@@ -288,31 +311,40 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
         }
       }
-      const float neg = m == -INFINITY ? 0.0f : -m * p.scale2;  // nothing attended yet: every p is exp2(-inf) = 0
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      const float neg = m == -INFINITY ? 0.0f : -m * p.scale2;  // nothing attended yet
+      const uint64_t neg2 = pair(neg, neg), scale2 = pair(p.scale2, p.scale2);
+      uint64_t sum[2] = {0, 0};
 #pragma unroll
-      for (int c = 0; c < 128; c += 64) {
-        uint32_t w[32];
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float a = ex2(fmaf(x[c + 2 * i], p.scale2, neg)), b = ex2(fmaf(x[c + 2 * i + 1], p.scale2, neg));
-          sum[(2 * i) & 3] += a;
-          sum[(2 * i + 1) & 3] += b;
-          w[i] = pack16<BF16>(a, b);
+        for (int i = 0; i < 16; ++i) {
+          float2 e = unpair(fma2(pair(x[c + 2 * i], x[c + 2 * i + 1]), scale2, neg2));
+          e.x = ex2(e.x);
+          e.y = ex2(e.y);
+          sum[i & 1] = add2(sum[i & 1], pair(e.x, e.y));
+          w[i] = pack16<BF16>(e.x, e.y);
         }
-        tmem_st32(ts + c / 2, w);
+        tmem_st16(ts + c / 2, w);
+        if (c == 64) {  // three quarters of P: the product can begin
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&p_most[t]);
+        }
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&p_full[t]);
+      const float2 total = unpair(add2(sum[0], sum[1]));
+      l += total.x + total.y;
     }
     if (good && nt > 0) {
       good = __all_sync(0xffffffffu, mbar_wait(&o_done[t], (nt - 1) & 1, abort_p, kPWait));
       tc_fence_after();
     }
     if (good && tok0 + t * tq < n_q) {
-      const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+      const bool attends = nt > 0 && lim >= 0 && m != -INFINITY;
+      const float inv = 1.0f / l;
       const bool store = tok < n_q;
       uint16_t* out = p.out + ((size_t)(job.q0 + tok) * p.n_heads + head) * HD;
       const bool fix = *(volatile int*)&dirty != 0;
@@ -325,7 +357,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         float y[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = nt > 0 && l != 0.0f ? __uint_as_float(o[i]) * inv : 0.0f;
+        for (int i = 0; i < 16; ++i) y[i] = attends ? __uint_as_float(o[i]) * inv : 0.0f;
         if (fix && store) {
           // the values that were taken out of V, for the positions that this row attends
           for (int pos = max(0, shift + tok0 + 1); pos <= lim; ++pos) {
@@ -347,7 +379,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     }
     tc_fence_before();
-  } else if (warp == 8) {
+  } else {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp == 8) {
     // ------------------------------------------------------------ products
     bool good = n > 0 && mbar_wait(&q_full, 0, abort_p, kPWait);
     good = __all_sync(0xffffffffu, good);
@@ -384,14 +418,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           // O_t += P_t V(j)
           if (!wait(&full[i % kSlots], (i / kSlots) & 1)) break;
           if (t == (j < n_t[0] ? 0 : 1) && j == dirty_from - 1 && lane == 0) mbar_arrive(&near);
-          if (j >= dirty_from && !wait(&clean, (j - dirty_from) & 1)) break;
+          if (j >= dirty_from && !wait(&clean[j % kVSlots], ((j - dirty_from) / kVSlots) & 1)) break;
+          const uint64_t b = sdesc_sw128(smem_addr(ring + (i % kSlots) * kOperand), kTile * 128, 1024);
+          auto product = [&](int k0, int k1) {
+#pragma unroll
+            for (int k = k0; k < k1; ++k)
+              mma_ts(tbase + 256 + t * HD, tbase + t * 128 + k * 8, b + (uint64_t)((k * 2048) >> 4), kIdO, (j | k) != 0);
+          };
+          if (!wait(&p_most[t], j & 1)) break;
+          tc_fence_after();
+          if (elect_one()) product(0, 6);
+          __syncwarp();
           if (!wait(&p_full[t], j & 1)) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t b = sdesc_sw128(smem_addr(ring + (i % kSlots) * kOperand), kTile * 128, 1024);
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              mma_ts(tbase + 256 + t * HD, tbase + t * 128 + k * 8, b + (uint64_t)((k * 2048) >> 4), kIdO, (j | k) != 0);
+            product(6, 8);
             mma_commit(&o_done[t]);
             if (t == 1 || j >= n_t[1]) mma_commit(&empty[i % kSlots]);
           }
@@ -461,8 +502,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(&clean);
+      mbar_arrive(&clean[j % kVSlots]);  // one barrier a slot: the cleaning may run ahead of the products
     }
+  }
   }
 
   __syncthreads();

@@ -311,6 +311,22 @@ def test_prompt_is_causal_whatever_later_positions_hold(tl, hd, page, dtype):
     assert torch.equal(out[:at], clean[:at]) and torch.isnan(out[at:]).all()
 
 
+def test_prompt_chunks_repeat_bit_for_bit(tl):
+    """Chunks over long caches, many CTAs with several tiles whose V is cleaned: the same bits every time."""
+    new = [512, 401, 300, 450]
+    total = [n + 4000 - 37 * b for b, n in enumerate(new)]
+    rig = Rig(tl, total, kv=4, group=4, hd=128, page=16, dtype=BF16, layers=1)
+    cu = np.cumsum([0] + new).tolist()
+    q = rig.queries(cu[-1])
+    first, out = torch.empty_like(q), torch.empty_like(q)
+    tl.paged_prompt_attn(rig.cache, 0, q, _i32(cu), _i32(total), first)
+    for _ in range(40):
+        out.fill_(float("nan"))
+        tl.paged_prompt_attn(rig.cache, 0, q, _i32(cu), _i32(total), out)
+        assert torch.equal(out, first)
+    rig.ok()
+
+
 def test_prompt_skips_and_reports(tl):
     rig = Rig(tl, [40, 40, 40, 40], kv=1, group=1, hd=64, page=16, dtype=FP16)
     rig.cache.table[1, 2] = -1
