@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   constexpr uint32_t kIdS = idesc16<BF16>(128, 128, false), kIdO = idesc16<BF16>(128, HD, true);
   static_assert(kSlots % 2 == 0, "V(j) lies in slot 2 (j mod kVSlots) + 1");
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t q_full, full[kSlots], empty[kSlots], s_full[2], p_most[2], p_full[2], o_done[2], near, clean[kVSlots], fin;
+  __shared__ uint64_t q_full, full[kSlots], empty[kSlots], s_full[2], p_full[2], o_done[2], near, clean[kVSlots], fin;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag, dirty;
   __shared__ Job job;
@@ -204,7 +204,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_most[t], 128);
       mbar_init(&p_full[t], 128);
       mbar_init(&o_done[t], 1);
     }
@@ -326,11 +325,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           w[i] = pack16<BF16>(e.x, e.y);
         }
         tmem_st16(ts + c / 2, w);
-        if (c == 64) {  // three quarters of P: the product can begin
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(&p_most[t]);
-        }
       }
       tmem_st_wait();
       tc_fence_before();
@@ -389,56 +383,51 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (good) good = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_p, kPWait));
       return good;
     };
+    const uint64_t q_desc[2] = {sdesc_sw128(smem_addr(qs), 16, 1024), sdesc_sw128(smem_addr(qs + kOperand), 16, 1024)};
     auto scores = [&](int t, int j) {  // S_t = Q_t K(j)^T
       const int i = 2 * j;
-      if (!wait(&full[i % kSlots], (i / kSlots) & 1)) return;
+      const uint64_t b = sdesc_sw128(smem_addr(ring + (i % kSlots) * kOperand), 16, 1024);
+#pragma unroll
+      for (int k = 0; k < HD / 16; ++k) {
+        const uint64_t off = (uint64_t)(((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4);
+        mma_ss(tbase + t * 128, q_desc[t] + off, b + off, kIdS, k != 0);
+      }
+      mma_commit(&s_full[t]);
+      if (t == 1 || j >= n_t[1]) mma_commit(&empty[i % kSlots]);
+    };
+    auto product = [&](int t, int j) {  // O_t += P_t V(j)
+      const int i = 2 * j + 1;
+      const uint64_t b = sdesc_sw128(smem_addr(ring + (i % kSlots) * kOperand), kTile * 128, 1024);
+#pragma unroll
+      for (int k = 0; k < kTile / 16; ++k)
+        mma_ts(tbase + 256 + t * HD, tbase + t * 128 + k * 8, b + (uint64_t)((k * 2048) >> 4), kIdO, (j | k) != 0);
+      mma_commit(&o_done[t]);
+      if (t == 1 || j >= n_t[1]) mma_commit(&empty[i % kSlots]);
+    };
+    if (good && wait(&full[0], 0)) {
       tc_fence_after();
       if (elect_one()) {
-        const uint64_t a = sdesc_sw128(smem_addr(qs + t * kOperand), 16, 1024);
-        const uint64_t b = sdesc_sw128(smem_addr(ring + (i % kSlots) * kOperand), 16, 1024);
-#pragma unroll
-        for (int k = 0; k < HD / 16; ++k) {
-          const uint64_t off = (uint64_t)(((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4);
-          mma_ss(tbase + t * 128, a + off, b + off, kIdS, k != 0);
-        }
-        mma_commit(&s_full[t]);
-        if (t == 1 || j >= n_t[1]) mma_commit(&empty[i % kSlots]);
+        if (n_t[0] > 0) scores(0, 0);
+        if (n_t[1] > 0) scores(1, 0);
       }
       __syncwarp();
       issued = true;
-    };
-    if (good) {
-      if (n_t[0] > 0) scores(0, 0);
-      if (good && n_t[1] > 0) scores(1, 0);
     }
     for (int j = 0; j < n && good; ++j) {
       const int i = 2 * j + 1;
-      for (int t = 0; t < 2 && good; ++t) {
-        if (j < n_t[t]) {
-          // O_t += P_t V(j)
-          if (!wait(&full[i % kSlots], (i / kSlots) & 1)) break;
-          if (t == (j < n_t[0] ? 0 : 1) && j == dirty_from - 1 && lane == 0) mbar_arrive(&near);
-          if (j >= dirty_from && !wait(&clean[j % kVSlots], ((j - dirty_from) / kVSlots) & 1)) break;
-          const uint64_t b = sdesc_sw128(smem_addr(ring + (i % kSlots) * kOperand), kTile * 128, 1024);
-          auto product = [&](int k0, int k1) {
-#pragma unroll
-            for (int k = k0; k < k1; ++k)
-              mma_ts(tbase + 256 + t * HD, tbase + t * 128 + k * 8, b + (uint64_t)((k * 2048) >> 4), kIdO, (j | k) != 0);
-          };
-          if (!wait(&p_most[t], j & 1)) break;
-          tc_fence_after();
-          if (elect_one()) product(0, 6);
-          __syncwarp();
-          if (!wait(&p_full[t], j & 1)) break;
-          tc_fence_after();
-          if (elect_one()) {
-            product(6, 8);
-            mma_commit(&o_done[t]);
-            if (t == 1 || j >= n_t[1]) mma_commit(&empty[i % kSlots]);
-          }
-          __syncwarp();
+      if (!wait(&full[i % kSlots], (i / kSlots) & 1)) break;
+      if (j == dirty_from - 1 && lane == 0) mbar_arrive(&near);
+      if (j >= dirty_from && !wait(&clean[j % kVSlots], ((j - dirty_from) / kVSlots) & 1)) break;
+      if (j + 1 < n && !wait(&full[(i + 1) % kSlots], ((i + 1) / kSlots) & 1)) break;
+      for (int t = 0; t < 2; ++t) {
+        if (j >= n_t[t]) continue;
+        if (!wait(&p_full[t], j & 1)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          product(t, j);
+          if (j + 1 < n_t[t]) scores(t, j + 1);
         }
-        if (j + 1 < n_t[t]) scores(t, j + 1);
+        __syncwarp();
       }
     }
   } else if (warp == 9) {
