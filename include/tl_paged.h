@@ -21,11 +21,11 @@
  * checked on the device: what is out of range is skipped as each call says and
  * TL_ERR_DEVICE_RANGE is recorded in the workspace's status word (tl_storeh_poll_status).
  *
- * Every call takes the workspace of tl_paged_workspace_bytes (256-byte aligned, its first 256
- * bytes, the status word, zeroed once).  Calls on one stream may share a workspace, and so may
- * captured graphs that are replayed one after the other; calls that may overlap on the GPU need
- * one each, except tl_paged_append and tl_paged_fork and tl_paged_free, which touch only the
- * status word.
+ * Every call takes the workspace of tl_paged_workspace_bytes (256-byte aligned, its first 4096
+ * bytes zeroed once; the status word is its first).  Calls on one stream may share a workspace,
+ * and so may captured graphs that are replayed one after the other; calls that may overlap on
+ * the GPU need one each, except tl_paged_append, tl_paged_fork and tl_paged_free, which touch
+ * only the status word.
  */
 #ifndef TL_PAGED_H_
 #define TL_PAGED_H_
@@ -76,7 +76,8 @@ TL_API tl_status tl_paged_cache_bytes(const tl_paged_desc* desc, size_t* pool_by
                                       size_t* refs_bytes);
 
 /* Workspace bytes for calls of up to n_lanes lanes (sequences) of n_heads query heads and split
- * length split_rows (see tl_paged_attn_decode), and for the operations on pages.
+ * length split_rows (see tl_paged_attn_decode), for prompt attention over any number of rows
+ * (59 MB at head_dim 128: partial results of 444 pieces) and for the operations on pages.
  * Errors: the desc errors, TL_ERR_INVALID_ARG (n_lanes, n_heads not positive, split_rows),
  * TL_ERR_SHAPE (n_heads not a multiple of n_kv_heads), TL_ERR_UNSUPPORTED (n_lanes > 1024,
  * n_heads > 1024). */

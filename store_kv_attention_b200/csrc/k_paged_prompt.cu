@@ -6,25 +6,31 @@
 // attended pair: the tensor pipe bounds long prompts, and next to it the exponentials (16 a clock and
 // SM: 1024 clocks per 128 x 128 tile, as many as its two products at hd = 128).
 //
-// One CTA takes two tiles of 128 query rows.  A row is a (token, head) pair: the Gp heads of one
+// Work: a block is two tiles of 128 query rows.  A row is a (token, head) pair: the Gp heads of one
 // K/V head that fit (Gp the largest power of two up to 128 dividing the group) lie next to each
-// other, 128 / Gp tokens a tile, so the heads of a group share their K and V tiles and the causal
-// edge is only 128 / Gp tokens wide.  Roles:
-//   warps 0-3, 4-7  softmax of tile 0 / 1, a thread per row: S from TMEM, maximum, P back into S's
-//                   columns as 16-bit values (A operand of the second product), at the end O / sum
-//   warp 8          issues the products: S_t(j+1) follows P_t(j) V(j), so that the tensor pipe
-//                   works on one tile while the other one's softmax runs
-//   warp 9          TMA producer: Q once, K and V tiles through a ring, page by page (a page of one
-//                   K/V head is one box per 64 values)
-//   warps 10-11     clean the V tiles that hold positions not every row attends: rows past the
-//                   cache's end are zeroed (their memory may hold anything) and values that are not
-//                   finite are taken out (0 x inf would reach the rows that do not attend them) and
-//                   given back in the epilogue to the rows that do
-// O is rescaled only when a row's maximum has grown by more than 2^8 in the exponent since the last
-// time (P and its sum stay below 2^8 x 128 tiles' worth of FP32): the exponent's base is a free
-// choice, and the rescale, a round trip of O through registers, becomes rare.
+// other, 128 / Gp tokens a tile, so the heads of a group share their K and V and the causal edge is
+// only 128 / Gp tokens wide.  Persistent CTAs, one per SM, take blocks from a counter, a lane's last
+// and longest first; when a call has too few blocks for the SMs, each is cut along its positions into
+// pieces whose (maximum, sum, O) are joined, in the order of the pieces, by the last one to finish.
 //
-// TMEM (512 columns): S_0 | S_1 (128 columns each; P over the first 64) | O_0 | O_1.
+// Positions come in steps of 64.  Roles of a CTA's warps:
+//   0-3, 4-7  softmax of tile 0 / 1, a thread per row: S from TMEM, maximum, P back over S's columns
+//             as 16-bit values (A operand of the second product), at the end O / sum
+//   8, 11     issue the products of tile 0 / 1 (a warp each: the waits of one, some 100 clocks even
+//             when there is nothing to wait for, pass behind the products of the other).  Each tile has
+//             two S buffers of 64 columns: S_t(u+2) is issued behind P_t(u) V(u), so that the next S
+//             is there while a tile's softmax runs and the tensor pipe has products meanwhile
+//   9         takes work and loads by TMA: Q once, K and V through two rings, page by page (a page of
+//             one K/V head is one box per 64 values)
+//   10        cleans the V steps that hold positions not every row attends: rows past the cache's end
+//             are zeroed (their memory may hold anything) and values that are not finite are taken
+//             out (0 x inf would reach the rows that do not attend them) and given back at the end
+//             to the rows that do
+// O is rescaled only when a row's maximum has grown by more than 2^8 in the exponent since the last
+// time: the base of the exponents is a free choice (P then reaches 2^8 and its sum 2^8 times the
+// positions, far inside FP32), and the rescale, a round trip of O through registers, becomes rare.
+//
+// TMEM (512 columns): S_0 (two buffers) | S_1 (128 columns each; P over a buffer's first 32) | O_0 | O_1.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -40,8 +46,10 @@ namespace {
 using namespace ptx;
 
 constexpr int kPromptThreads = 384;
-constexpr int kTile = 128;
-constexpr long long kPWait = 4000000000ll;
+constexpr int kTile = 128;                // query rows of a tile
+constexpr int kStep = 64;                 // positions of a step
+constexpr int kSms = 148;
+constexpr long long kPWait = 4000000000ll;  // SM clocks
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.0f;  // growth of the maximum, in powers of two, that O is rescaled for
 
@@ -54,15 +62,19 @@ struct PromptParams {
   const int32_t* seqs;
   uint16_t* out;
   uint32_t* status;
-  float scale2;  // scale * log2 e
-  int n_heads, group, pack, n_rows, n_lanes;
+  int32_t* queue;     // [0]: blocks taken beyond the first of each CTA, [1]: CTAs done; both 0 between calls
+  int32_t* finished;  // [kPromptPieces][2] pieces of a block that are done, per tile; 0 between calls
+  float* part;        // [kPromptPieces][2] x (maximum and sum [128][2] | O [HD][128])
+  float scale2;       // scale * log2 e
+  int n_heads, group, pack, n_rows, n_lanes, pieces;
 };
 
 template <int HD>
 struct PromptSmem {
-  static constexpr int kOperand = kTile * HD * 2;  // one tile of Q, K or V
-  static constexpr int kSlots = HD == 128 ? 4 : 8;
-  static constexpr int kBytes = 1024 + (2 + kSlots) * kOperand;
+  static constexpr int kQ = kTile * HD * 2;     // one tile of queries
+  static constexpr int kKv = kStep * HD * 2;    // one step of K or of V
+  static constexpr int kSlots = 4;              // of each ring
+  static constexpr int kBytes = 1024 + 2 * kQ + 2 * kSlots * kKv;
 };
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
@@ -127,111 +139,71 @@ __host__ __device__ constexpr uint32_t idesc16(int M, int N, bool b_mn_major) {
   return idesc_f16_f32(M, N, false, b_mn_major) | (BF16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
-// What one CTA works on, worked out by warp 0 and shared.
+// What a CTA works on.
 struct Job {
-  int lane;        // -1: nothing to do
-  int q0, n_q;     // first packed row and number of queries of the lane
-  int kv, seq;     // cached positions, sequence
-  int tok0;        // first token of the CTA's first tile
+  int lane;     // -1: no more
+  int q0, n_q;  // first packed row and number of queries of the lane
+  int kv, seq;  // cached positions, sequence
+  int tok0;     // first token of the first tile
+  int head0, kvh;
+  int u0, n;    // first step of the piece, steps
+  int n_t[2];   // of them, those that tile t attends
+  int dirty_from;  // first step of the piece with positions that not every row attends
+  int slot, piece, pieces;  // where partial results go: (block, heads) and piece
+  int dirty;    // a value that is not finite was taken out of V
 };
-
-// Block `blk` of the lanes' blocks of 2 x tq tokens, a lane's last block first (the longest).
-__device__ void find_job(const PromptParams& p, int blk, int tq, Job* job) {
-  const int lane = threadIdx.x & 31;
-  int found = -1, done = 0;
-  for (int base = 0; base < p.n_lanes && (found < 0 || blk == 0); base += 32) {
-    const int b = base + lane;
-    int n = 0, q0 = 0, blocks = 0;
-    if (b < p.n_lanes) {
-      q0 = p.cu_q[b];
-      const int q1 = p.cu_q[b + 1];
-      n = q1 - q0;
-      if (q0 < 0 || q1 > p.n_rows || n < 0) {
-        if (blk == 0) atomicOr(p.status, kStatusRange);
-        n = 0;
-      }
-      blocks = (n + 2 * tq - 1) / (2 * tq);
-    }
-    int incl = blocks;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    const unsigned has = __ballot_sync(0xffffffffu, blocks > 0 && blk < done + incl && blk >= done + incl - blocks);
-    if (has && found < 0) {
-      const int l = __ffs(has) - 1;
-      found = base + l;
-      if (lane == l) {
-        const int seq = p.seqs ? p.seqs[b] : b, kv = p.kv_len[b];
-        const bool ok = seq >= 0 && seq < p.s.max_seqs && kv >= 0 && kv <= p.s.max_len();
-        if (!ok) atomicOr(p.status, kStatusRange);
-        *job = Job{ok ? b : -1, q0, n, kv, seq, (done + incl - 1 - blk) * 2 * tq};
-      }
-    }
-    done += __shfl_sync(0xffffffffu, incl, 31);
-  }
-  if (found < 0 && lane == 0) job->lane = -1;
-}
 
 template <int HD, bool BF16>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     paged_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const PromptParams p) {
-  constexpr int kOperand = PromptSmem<HD>::kOperand, kSlots = PromptSmem<HD>::kSlots, kVSlots = kSlots / 2;
-  constexpr uint32_t kIdS = idesc16<BF16>(128, 128, false), kIdO = idesc16<BF16>(128, HD, true);
-  static_assert(kSlots % 2 == 0, "V(j) lies in slot 2 (j mod kVSlots) + 1");
+  using Smem = PromptSmem<HD>;
+  constexpr int kSlots = Smem::kSlots;
+  constexpr uint32_t kIdS = idesc16<BF16>(128, kStep, false), kIdO = idesc16<BF16>(128, HD, true);
+  constexpr int kPartFloats = kTile * (HD + 2);
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t q_full, full[kSlots], empty[kSlots], s_full[2], p_full[2], o_done[2], near, clean[kVSlots], fin;
+  // A wait by parity cannot tell a phase from the second one behind it, so every barrier is waited for in
+  // each of its phases in turn, or its next phase needs the waiter; what may be two steps behind has two.
+  __shared__ uint64_t q_full, q_empty, k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots], v_clean[kSlots];
+  __shared__ uint64_t s_full[2][2], p_full[2][2], o_done[2][2], job_full[2], job_empty[2], part_done[2], part_said[2], fin[2];
   __shared__ uint32_t tmem_base;
-  __shared__ int abort_flag, dirty;
-  __shared__ Job job;
-  uint8_t* base = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-  uint8_t* qs = base;                  // two tiles
-  uint8_t* ring = base + 2 * kOperand;  // K(0), V(0), K(1), V(1), ...
+  __shared__ int abort_flag, v_seen, last_piece[2];
+  __shared__ Job jobs[2];
+  __shared__ int first_block[kPagedMaxLanes + 1];  // of each lane
+  uint8_t* qs = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);  // two tiles
+  uint8_t* ks = qs + 2 * Smem::kQ;
+  uint8_t* vs = ks + kSlots * Smem::kKv;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PagedShape& s = p.s;
-  pdl_wait();
-  const int subs = p.n_heads / p.pack, sub = blockIdx.x % subs, tq = kTile / p.pack;
-  const int h0 = sub * p.pack, kvh = h0 / p.group;
-  if (warp == 0) find_job(p, blockIdx.x / subs, tq, &job);
-  if (threadIdx.x == 32) {
+  const int subs = p.n_heads / p.pack, tq = kTile / p.pack;
+  if (threadIdx.x == 0) {
     mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 2);
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 2);  // both tiles
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 2);
+      mbar_init(&v_clean[i], 32);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 128);
-      mbar_init(&o_done[t], 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&s_full[t][i], 1);
+        mbar_init(&p_full[t][i], 128);
+        mbar_init(&o_done[t][i], 1);
+      }
+      mbar_init(&fin[t], 1);
+      mbar_init(&part_done[t], 128);
+      mbar_init(&part_said[t], 1);
+      mbar_init(&job_full[t], 1);
+      mbar_init(&job_empty[t], 11);  // warps that read a job
     }
-    mbar_init(&near, 1);
-    for (int i = 0; i < kVSlots; ++i) mbar_init(&clean[i], 64);
-    mbar_init(&fin, 1);
     abort_flag = 0;
-    dirty = 0;
+    v_seen = 0;
     mbar_fence_init();
   }
-  __syncthreads();
-  if (job.lane < 0) {
-    pdl_trigger();
-    return;
-  }
-  const int n_q = job.n_q, kv_len = job.kv, tok0 = job.tok0;
-  const int32_t* row = p.table + (size_t)job.seq * s.max_pages;
-  // every page of the lane has to be one of the pool
-  bool ok = true;
-  for (int j = threadIdx.x; j < (kv_len + s.page - 1) / s.page; j += kPromptThreads) {
-    const int pg = row[j];
-    ok = ok && pg >= 0 && pg < s.n_pages;
-  }
-  if (!__syncthreads_and(ok)) {
-    if (threadIdx.x == 0) atomicOr(p.status, kStatusRange);
-    pdl_trigger();
-    return;
-  }
+  pdl_wait();
   if (warp == 8) {
     tmem_alloc(&tmem_base, 512);
     tmem_relinquish();
@@ -242,258 +214,505 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const uint32_t tbase = tmem_base;
   volatile int* abort_p = &abort_flag;
   pdl_trigger();  // TMEM is held
+  bool issued = false;                 // products issued (warps 8, 11)
+  int q_loads = 0, k_loads = 0, v_loads = 0;  // (warp 9)
 
-  const int shift = kv_len - n_q;  // position of token 0
-  // K/V tiles each query tile needs, by its last token's position
-  int n_t[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int first = tok0 + t * tq, last = min(n_q, first + tq) - 1;
-    n_t[t] = first < n_q && shift + last >= 0 ? (shift + last) / kTile + 1 : 0;
-  }
-  const int n = max(n_t[0], n_t[1]);
-  const int dirty_from = max(0, shift + tok0 + 1) / kTile;  // first tile with positions that not every row attends
-  int loads = 0;                                            // ring loads issued (producer warp)
-  bool issued = false;                                      // products issued (warp 8)
-
-  // Registers: 384 x 168 at launch = 256 x 208 + 128 x 88.  A softmax thread holds a row of S.
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ------------------------------------------------------------ softmax of tile t, row r
     const int t = warp >> 2, r = threadIdx.x & 127;
-    const int tok = tok0 + t * tq + r / p.pack, head = h0 + r % p.pack;
-    const int lim = min(shift + tok, kv_len - 1);                     // last attended position
-    const int sure = shift + tok0 + t * tq;                           // attended by every row of the tile
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tbase + lanes + t * 128, to = tbase + lanes + 256 + t * HD;
-    const int nt = n_t[t];
-    float m = -INFINITY, l = 0.0f;  // m: the base of the exponents
+    int c = 0, parts = 0;  // steps of this tile and partial results so far
     bool good = true;
-    for (int j = 0; j < nt; ++j) {
-      if (!(good = __all_sync(0xffffffffu, mbar_wait(&s_full[t], j & 1, abort_p, kPWait)))) break;
-      tc_fence_after();
-      float x[128];
+    for (int nj = 0; good; ++nj) {
+      if (!(good = __all_sync(0xffffffffu, mbar_wait(&job_full[nj & 1], (nj >> 1) & 1, abort_p, kPWait)))) break;
+      const Job& job = jobs[nj & 1];
+      if (job.lane < 0) break;
+      const int first = job.tok0 + t * tq, shift = job.kv - job.n_q;  // shift: position of token 0
+      const int tok = first + r / p.pack, head = job.head0 + r % p.pack;
+      const int lim = min(shift + tok, job.kv - 1);  // last attended position
+      const int sure = shift + first;                // attended by every row of the tile
+      const int nt = job.n_t[t], pos0 = job.u0 * kStep;
+      float m = -INFINITY, l = 0.0f;  // m: the base of the exponents
+      for (int u = 0; u < nt; ++u, ++c) {
+        const int buf = c & 1;
+        if (!(good = __all_sync(0xffffffffu, mbar_wait(&s_full[t][buf], (c >> 1) & 1, abort_p, kPWait)))) break;
+        tc_fence_after();
+        float x[kStep];
+        tmem_ld32(ts + buf * kStep, reinterpret_cast<uint32_t*>(x));
+        tmem_ld32(ts + buf * kStep + 32, reinterpret_cast<uint32_t*>(x) + 32);
+        tmem_ld_wait();
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, reinterpret_cast<uint32_t*>(x) + c * 32);
-      tmem_ld_wait();
-      if (j * kTile + kTile - 1 > sure) {
+        for (int i = 0; i < kStep; ++i) asm volatile("" : "+f"(x[i]));  // nothing of x is used before the wait
+        const int pos = pos0 + u * kStep;
+        if (pos + kStep - 1 > sure) {
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (j * kTile + c > lim) x[c] = -INFINITY;
-      }
-      float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-      for (int c = 4; c < 128; ++c) asm("max.NaN.f32 %0, %0, %1;" : "+f"(mx[c & 3]) : "f"(x[c]));
-      float top = mx[0];
-#pragma unroll
-      for (int c = 1; c < 4; ++c) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(mx[c]));
-      const bool grown = !((top - m) * p.scale2 <= kGrow);  // not comparable: a NaN, or nothing attended yet
-      if (__any_sync(0xffffffffu, grown)) {
-        float f = 1.0f;  // a row's result does not depend on the rows beside it
-        if (grown) {
-          const float was = m;
-          asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(top));
-          f = was == -INFINITY ? 0.0f : ex2((was - m) * p.scale2);
-          l *= f;
+          for (int i = 0; i < kStep; ++i)
+            if (pos + i > lim) x[i] = -INFINITY;
         }
-        if (j > 0) {
-          if (!(good = __all_sync(0xffffffffu, mbar_wait(&o_done[t], (j - 1) & 1, abort_p, kPWait)))) break;
-          tc_fence_after();
+        float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int c = 0; c < HD; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(to + c, o);
-            tmem_ld_wait();
+        for (int i = 4; i < kStep; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(mx[i & 3]) : "f"(x[i]));
+        float top = mx[0];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st16(to + c, o);
+        for (int i = 1; i < 4; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(mx[i]));
+        const bool grown = !((top - m) * p.scale2 <= kGrow);  // not comparable: a NaN, or nothing attended yet
+        if (__any_sync(0xffffffffu, grown)) {
+          float f = 1.0f;  // a row's result does not depend on the rows beside it
+          if (grown) {
+            const float was = m;
+            asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(top));
+            f = was == -INFINITY ? 0.0f : ex2((was - m) * p.scale2);
+            l *= f;
           }
-        }
-      }
-      const float neg = m == -INFINITY ? 0.0f : -m * p.scale2;  // nothing attended yet
-      const uint64_t neg2 = pair(neg, neg), scale2 = pair(p.scale2, p.scale2);
-      uint64_t sum[2] = {0, 0};
+          if (u > 0) {
+            if (!(good = __all_sync(0xffffffffu, mbar_wait(&o_done[t][(c - 1) & 1], ((c - 1) >> 1) & 1, abort_p, kPWait)))) break;
+            tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < 128; c += 32) {
-        uint32_t w[16];
+            for (int d = 0; d < HD; d += 16) {
+              uint32_t o[16];
+              tmem_ld16(to + d, o);
+              tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float2 e = unpair(fma2(pair(x[c + 2 * i], x[c + 2 * i + 1]), scale2, neg2));
-          e.x = ex2(e.x);
-          e.y = ex2(e.y);
-          sum[i & 1] = add2(sum[i & 1], pair(e.x, e.y));
-          w[i] = pack16<BF16>(e.x, e.y);
-        }
-        tmem_st16(ts + c / 2, w);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&p_full[t]);
-      const float2 total = unpair(add2(sum[0], sum[1]));
-      l += total.x + total.y;
-    }
-    if (good && nt > 0) {
-      good = __all_sync(0xffffffffu, mbar_wait(&o_done[t], (nt - 1) & 1, abort_p, kPWait));
-      tc_fence_after();
-    }
-    if (good && tok0 + t * tq < n_q) {
-      const bool attends = nt > 0 && lim >= 0 && m != -INFINITY;
-      const float inv = 1.0f / l;
-      const bool store = tok < n_q;
-      uint16_t* out = p.out + ((size_t)(job.q0 + tok) * p.n_heads + head) * HD;
-      const bool fix = *(volatile int*)&dirty != 0;
-#pragma unroll
-      for (int c = 0; c < HD; c += 16) {
-        uint32_t o[16];
-        if (nt > 0) {  // warp-uniform
-          tmem_ld16(to + c, o);
-          tmem_ld_wait();
-        }
-        float y[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = attends ? __uint_as_float(o[i]) * inv : 0.0f;
-        if (fix && store) {
-          // the values that were taken out of V, for the positions that this row attends
-          for (int pos = max(0, shift + tok0 + 1); pos <= lim; ++pos) {
-            const uint16_t* src = p.v + ((size_t)row[pos / s.page] * s.kv + kvh) * s.block_elems() + (size_t)(pos % s.page) * HD + c;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float v = unpack16<BF16>(src[i]);
-              if (!isfinite(v)) y[i] += v;
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st16(to + d, o);
             }
           }
         }
-        if (store) {
-          uint32_t w[8];
+        const float neg = m == -INFINITY ? 0.0f : -m * p.scale2;  // nothing attended yet
+        const uint64_t neg2 = pair(neg, neg), scale2 = pair(p.scale2, p.scale2);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = pack16<BF16>(y[2 * i], y[2 * i + 1]);
-          *reinterpret_cast<uint4*>(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+        for (int d = 0; d < kStep; d += 32) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float2 e = unpair(fma2(pair(x[d + 2 * i], x[d + 2 * i + 1]), scale2, neg2));
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            sum[i & 1] = add2(sum[i & 1], pair(e.x, e.y));
+            w[i] = pack16<BF16>(e.x, e.y);
+          }
+          tmem_st16(ts + buf * kStep + d / 2, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_full[t][buf]);
+        const float2 total = unpair(add2(sum[0], sum[1]));
+        l += total.x + total.y;
+      }
+      if (good && nt > 0) {
+        good = __all_sync(0xffffffffu, mbar_wait(&o_done[t][(c - 1) & 1], ((c - 1) >> 1) & 1, abort_p, kPWait));
+        tc_fence_after();
+      }
+      if (!good) break;
+      const bool attends = nt > 0 && lim >= 0 && m != -INFINITY;
+      const bool store = tok < job.n_q;
+      const int fix0 = max(max(0, shift + job.tok0 + 1), pos0), fix1 = min(lim, pos0 + job.n * kStep - 1);
+      const bool fix = *(volatile const int*)&job.dirty != 0 && store;
+      const int32_t* row = p.table + (size_t)job.seq * s.max_pages;
+      // the values that were taken out of V, for the positions that this row attends
+      auto give_back = [&](int d, float* y) {
+        for (int pos = fix0; pos <= fix1; ++pos) {
+          const uint16_t* src = p.v + ((size_t)row[pos / s.page] * s.kv + job.kvh) * s.block_elems() + (size_t)(pos % s.page) * HD + d;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float v = unpack16<BF16>(src[i]);
+            if (!isfinite(v)) y[i] += v;
+          }
+        }
+      };
+      uint16_t* out = p.out + ((size_t)(job.q0 + tok) * p.n_heads + head) * HD;
+      if (job.pieces == 1) {
+        const float inv = 1.0f / l;
+        if (first < job.n_q) {
+#pragma unroll
+          for (int d = 0; d < HD; d += 16) {
+            uint32_t o[16];
+            if (nt > 0) {  // warp-uniform
+              tmem_ld16(to + d, o);
+              tmem_ld_wait();
+            }
+            float y[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = attends ? __uint_as_float(o[i]) * inv : 0.0f;
+            if (fix) give_back(d, y);
+            if (store) {
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[i] = pack16<BF16>(y[2 * i], y[2 * i + 1]);
+              *reinterpret_cast<uint4*>(out + d) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(out + d + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
+        }
+      } else if (first < job.n_q) {
+        // leave the piece's part; the last piece of the tile to come by joins them all in their order
+        float* part = p.part + ((size_t)(job.slot + job.piece) * 2 + t) * kPartFloats;
+        reinterpret_cast<float2*>(part)[r] = make_float2(attends ? m : -INFINITY, l);
+        if (nt > 0) {
+#pragma unroll
+          for (int d = 0; d < HD; d += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + d, o);
+            tmem_ld_wait();
+            float y[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(o[i]);
+            if (fix) give_back(d, y);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) part[2 * kTile + (d + i) * kTile + r] = y[i];
+          }
+        }
+        __threadfence();
+        mbar_arrive(&part_done[t]);
+        if (r == 0 && (good = mbar_wait(&part_done[t], parts & 1, abort_p, kPWait))) {
+          __threadfence();
+          int32_t* count = p.finished + job.slot * 2 + t;
+          const bool last = atomicAdd(count, 1) == job.pieces - 1;
+          if (last) *count = 0;
+          last_piece[t] = last;
+          mbar_arrive(&part_said[t]);
+        }
+        good = __all_sync(0xffffffffu, good && mbar_wait(&part_said[t], parts & 1, abort_p, kPWait));
+        if (!good) break;
+        ++parts;
+        if (*(volatile int*)&last_piece[t]) {
+          __threadfence();
+          const float* base = p.part + ((size_t)job.slot * 2 + t) * kPartFloats;
+          const size_t next = 2 * kPartFloats;  // the following piece's
+          float f[kPromptMostPieces], top = -INFINITY, sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < kPromptMostPieces; ++i) {
+            f[i] = i < job.pieces ? __ldcg(base + i * next + 2 * r) : -INFINITY;
+            top = fmaxf(top, f[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < kPromptMostPieces; ++i) {
+            // a NaN stays one; a piece of which the row attends nothing counts for nothing
+            f[i] = f[i] == -INFINITY ? 0.0f : ex2((f[i] - top) * p.scale2);
+            if (f[i] != 0.0f) sum = fmaf(__ldcg(base + i * next + 2 * r + 1), f[i], sum);
+          }
+          const float inv = 1.0f / sum;
+          if (store)
+            for (int d = 0; d < HD; d += 8) {
+              float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+              for (int i = 0; i < kPromptMostPieces; ++i)
+                if (f[i] != 0.0f) {
+#pragma unroll
+                  for (int k = 0; k < 8; ++k)
+                    y[k] = fmaf(__ldcg(base + i * next + 2 * kTile + (d + k) * kTile + r), f[i], y[k]);
+                }
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = top == -INFINITY ? 0u : pack16<BF16>(y[2 * k] * inv, y[2 * k + 1] * inv);
+              *reinterpret_cast<uint4*>(out + d) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&job_empty[nj & 1]);
     }
-    tc_fence_before();
-  } else {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp == 8) {
-    // ------------------------------------------------------------ products
-    bool good = n > 0 && mbar_wait(&q_full, 0, abort_p, kPWait);
-    good = __all_sync(0xffffffffu, good);
+  } else if (warp == 8 || warp == 11) {
+    // ------------------------------------------------------------ products of tile t
+    const int t = warp == 11;
+    bool good = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (good) good = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_p, kPWait));
       return good;
     };
-    const uint64_t q_desc[2] = {sdesc_sw128(smem_addr(qs), 16, 1024), sdesc_sw128(smem_addr(qs + kOperand), 16, 1024)};
-    auto scores = [&](int t, int j) {  // S_t = Q_t K(j)^T
-      const int i = 2 * j;
-      const uint64_t b = sdesc_sw128(smem_addr(ring + (i % kSlots) * kOperand), 16, 1024);
-#pragma unroll
-      for (int k = 0; k < HD / 16; ++k) {
-        const uint64_t off = (uint64_t)(((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4);
-        mma_ss(tbase + t * 128, q_desc[t] + off, b + off, kIdS, k != 0);
-      }
-      mma_commit(&s_full[t]);
-      if (t == 1 || j >= n_t[1]) mma_commit(&empty[i % kSlots]);
-    };
-    auto product = [&](int t, int j) {  // O_t += P_t V(j)
-      const int i = 2 * j + 1;
-      const uint64_t b = sdesc_sw128(smem_addr(ring + (i % kSlots) * kOperand), kTile * 128, 1024);
-#pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
-        mma_ts(tbase + 256 + t * HD, tbase + t * 128 + k * 8, b + (uint64_t)((k * 2048) >> 4), kIdO, (j | k) != 0);
-      mma_commit(&o_done[t]);
-      if (t == 1 || j >= n_t[1]) mma_commit(&empty[i % kSlots]);
-    };
-    if (good && wait(&full[0], 0)) {
-      tc_fence_after();
-      if (elect_one()) {
-        if (n_t[0] > 0) scores(0, 0);
-        if (n_t[1] > 0) scores(1, 0);
-      }
+    const uint64_t q_desc = sdesc_sw128(smem_addr(qs + t * Smem::kQ), 16, 1024);
+    const uint64_t k_desc = sdesc_sw128(smem_addr(ks), 16, 1024), v_desc = sdesc_sw128(smem_addr(vs), kStep * 128, 1024);
+    const uint32_t ts = tbase + t * 128, to = tbase + 256 + t * HD;
+    int kv = 0, c = 0;         // steps of K and V, and of this tile, before this job
+    uint32_t clean_phase = 0;  // one bit per V slot
+    for (int nj = 0; good; ++nj) {
+      if (!wait(&job_full[nj & 1], (nj >> 1) & 1)) break;
+      const Job& job = jobs[nj & 1];
+      if (job.lane < 0) break;
+      const int n = job.n, nt = job.n_t[t], dirty_from = job.dirty_from;
       __syncwarp();
-      issued = true;
-    }
-    for (int j = 0; j < n && good; ++j) {
-      const int i = 2 * j + 1;
-      if (!wait(&full[i % kSlots], (i / kSlots) & 1)) break;
-      if (j == dirty_from - 1 && lane == 0) mbar_arrive(&near);
-      if (j >= dirty_from && !wait(&clean[j % kVSlots], ((j - dirty_from) / kVSlots) & 1)) break;
-      if (j + 1 < n && !wait(&full[(i + 1) % kSlots], ((i + 1) / kSlots) & 1)) break;
-      for (int t = 0; t < 2; ++t) {
-        if (j >= n_t[t]) continue;
-        if (!wait(&p_full[t], j & 1)) break;
-        tc_fence_after();
-        if (elect_one()) {
-          product(t, j);
-          if (j + 1 < n_t[t]) scores(t, j + 1);
+      if (lane == 0) mbar_arrive(&job_empty[nj & 1]);
+      auto scores = [&](int u) {  // S_t(u) = Q_t K(u)^T
+        const int slot = (kv + u) % kSlots, buf = (c + u) & 1;
+        const uint64_t b = k_desc + (uint64_t)((slot * Smem::kKv) >> 4);
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k)
+          mma_ss(ts + buf * kStep, q_desc + (uint64_t)(((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4),
+                 b + (uint64_t)(((k / 4) * (kStep * 128) + (k % 4) * 32) >> 4), kIdS, k != 0);
+        mma_commit(&s_full[t][buf]);
+        mma_commit(&k_empty[slot]);
+        if (u == n - 1) mma_commit(&q_empty);
+      };
+      auto product = [&](int u) {  // O_t += P_t(u) V(u)
+        const int slot = (kv + u) % kSlots, buf = (c + u) & 1;
+        const uint64_t b = v_desc + (uint64_t)((slot * Smem::kKv) >> 4);
+#pragma unroll
+        for (int k = 0; k < kStep / 16; ++k)
+          mma_ts(to, ts + buf * kStep + k * 8, b + (uint64_t)((k * 2048) >> 4), kIdO, (u | k) != 0);
+        mma_commit(&o_done[t][buf]);
+        mma_commit(&v_empty[slot]);
+      };
+      // steps that this tile does not attend: their slots (and the queries) are given back unread
+      auto pass_k = [&](int u) {
+        if (lane == 0) {
+          mbar_arrive(&k_empty[(kv + u) % kSlots]);
+          if (u == n - 1) mbar_arrive(&q_empty);
         }
+      };
+      if (n > 0 && !wait(&q_full, nj & 1)) break;
+      for (int u = 0; u < 2 && u < n; ++u) {
+        if (!wait(&k_full[(kv + u) % kSlots], ((kv + u) / kSlots) & 1)) break;
+        tc_fence_after();
+        if (u >= nt)
+          pass_k(u);
+        else if (elect_one())
+          scores(u);
+        __syncwarp();
+        issued = true;
+      }
+      for (int u = 0; u < n && good; ++u) {
+        const int slot = (kv + u) % kSlots;
+        if (!wait(&v_full[slot], ((kv + u) / kSlots) & 1)) break;
+        if (t == 0 && lane == 0) *(volatile int*)&v_seen = kv + u + 1;
+        if (u >= dirty_from) {
+          if (!wait(&v_clean[slot], (clean_phase >> slot) & 1)) break;
+          clean_phase ^= 1u << slot;
+        }
+        if (u + 2 < n && !wait(&k_full[(kv + u + 2) % kSlots], ((kv + u + 2) / kSlots) & 1)) break;
+        if (u < nt) {
+          if (!wait(&p_full[t][(c + u) & 1], ((c + u) >> 1) & 1)) break;
+          tc_fence_after();
+          if (elect_one()) {
+            product(u);
+            if (u + 2 < nt) scores(u + 2);
+          }
+        } else if (lane == 0) {
+          mbar_arrive(&v_empty[slot]);
+        }
+        if (u + 2 < n && u + 2 >= nt) pass_k(u + 2);
         __syncwarp();
       }
+      kv += n;
+      c += nt;
     }
   } else if (warp == 9) {
-    // ------------------------------------------------------------ loads
-    const int per = kTile / s.page;  // pages of a tile
-    if (n > 0) {
+    // ------------------------------------------------------------ work and loads
+    // the lanes' blocks of 2 x tq tokens
+    int blocks = 0;
+    for (int base = 0; base < p.n_lanes; base += 32) {
+      const int b = base + lane;
+      int n = 0;
+      if (b < p.n_lanes) {
+        const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
+        if (q0 < 0 || q1 > p.n_rows || q1 < q0) {
+          if (blockIdx.x == 0) atomicOr(p.status, kStatusRange);
+        } else {
+          n = (q1 - q0 + 2 * tq - 1) / (2 * tq);
+        }
+      }
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (b < p.n_lanes) first_block[b] = blocks + incl - n;
+      blocks += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) first_block[p.n_lanes] = blocks;
+    __syncwarp();
+    const int items = blocks * subs * p.pieces;
+    const int box = min(s.page, kStep), per = kStep / box;  // rows of a TMA box, boxes of a step
+    const int wide = s.page / box - 1;                      // 1: a page is two boxes (128 positions)
+    bool good = true;
+    int taken = blockIdx.x, kv_loads = 0;
+    for (int nj = 0; good;) {
+      const int item = taken;
+      if (item < items) {
+        int next = 0;
+        if (lane == 0) next = gridDim.x + atomicAdd(p.queue, 1);
+        taken = __shfl_sync(0xffffffffu, next, 0);
+      }
+      Job job = {};
+      job.lane = -1;
+      const int32_t* row = nullptr;
+      if (item < items) {
+        const int piece = item % p.pieces, bs = item / p.pieces, sub = bs % subs, blk = bs / subs;
+        int lo = 0, hi = p.n_lanes;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (first_block[mid] <= blk)
+            lo = mid;
+          else
+            hi = mid;
+        }
+        job.lane = lo;
+        job.q0 = p.cu_q[lo];
+        job.n_q = p.cu_q[lo + 1] - job.q0;
+        job.kv = p.kv_len[lo];
+        job.seq = p.seqs ? p.seqs[lo] : lo;
+        bool ok = job.seq >= 0 && job.seq < s.max_seqs && job.kv >= 0 && job.kv <= s.max_len();
+        if (ok) {
+          // every position of the lane has to have a page of the pool
+          row = p.table + (size_t)job.seq * s.max_pages;
+          const int held = (job.kv + s.page - 1) / s.page;
+#pragma unroll 4
+          for (int j = lane; j < held; j += 32) {
+            const int pg = row[j];
+            ok = ok && pg >= 0 && pg < s.n_pages;
+          }
+        }
+        if (!__all_sync(0xffffffffu, ok)) {
+          if (lane == 0) atomicOr(p.status, kStatusRange);
+          continue;
+        }
+        job.tok0 = (first_block[lo + 1] - 1 - blk) * 2 * tq;  // a lane's last block first
+        job.head0 = sub * p.pack;
+        job.kvh = job.head0 / p.group;
+        const int shift = job.kv - job.n_q;
+        int n_t[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          // steps a tile needs, by its last token's position
+          const int first = job.tok0 + t * tq, last = shift + min(job.n_q, first + tq) - 1;
+          n_t[t] = first < job.n_q && last >= 0 ? last / kStep + 1 : 0;
+        }
+        const int all = max(n_t[0], n_t[1]);
+        job.pieces = max(1, min(p.pieces, all / kPieceSteps));
+        const int each = (all + job.pieces - 1) / job.pieces;
+        if (piece >= job.pieces) continue;
+        job.piece = piece;
+        job.slot = bs * p.pieces;
+        job.u0 = piece * each;
+        job.n = max(0, min(each, all - job.u0));
+        for (int t = 0; t < 2; ++t) job.n_t[t] = max(0, min(job.n, n_t[t] - job.u0));
+        job.dirty_from = max(0, max(0, shift + job.tok0 + 1) / kStep - job.u0);
+      }
+      if (nj >= 2) good = __all_sync(0xffffffffu, mbar_wait(&job_empty[nj & 1], ((nj >> 1) - 1) & 1, abort_p, kPWait));
+      if (!good) break;
       if (lane == 0) {
-        mbar_expect_tx(&q_full, 2 * kOperand);
+        jobs[nj & 1] = job;
+        mbar_arrive(&job_full[nj & 1]);
+      }
+      __syncwarp();
+      if (job.lane < 0) break;
+      const int n = job.n;
+      if (n == 0) {
+        // q_full's and q_empty's phases go by jobs: an empty one passes its turn on
+        if (nj > 0 && !(good = __all_sync(0xffffffffu, mbar_wait(&q_empty, (nj - 1) & 1, abort_p, kPWait)))) break;
+        if (lane == 0) {
+          mbar_arrive(&q_full);
+          mbar_arrive(&q_empty);
+          mbar_arrive(&q_empty);
+        }
+        ++nj;
+        continue;
+      }
+      if (nj > 0 && !(good = __all_sync(0xffffffffu, mbar_wait(&q_empty, (nj - 1) & 1, abort_p, kPWait)))) break;
+      if (lane == 0) {
+        mbar_expect_tx(&q_full, 2 * Smem::kQ);
         for (int t = 0; t < 2; ++t)
           for (int h = 0; h < HD / 64; ++h)
-            tma_load_3d(qs + t * kOperand + h * (kTile * 128), &tmQ, h * 64, h0, job.q0 + tok0 + t * tq, &q_full);
+            tma_load_3d(qs + t * Smem::kQ + h * (kTile * 128), &tmQ, h * 64, job.head0, job.q0 + job.tok0 + t * tq, &q_full);
       }
-      bool good = true;
-      for (int j = 0; j < n && good; ++j) {
-        const int pos = j * kTile + lane * s.page;
-        const int pg = lane < per && pos < kv_len ? row[pos / s.page] : -1;
-        const int held = __popc(__ballot_sync(0xffffffffu, pg >= 0));
-        for (int kv = 0; kv < 2 && good; ++kv) {
-          const int i = 2 * j + kv, slot = i % kSlots;
-          if (i >= kSlots) good = __all_sync(0xffffffffu, mbar_wait(&empty[slot], (i / kSlots - 1) & 1, abort_p, kPWait));
+      q_loads = ++nj;
+      // pages of 32 boxes at a time, one per lane, and of the 32 behind them
+      const int box0 = job.u0 * per;
+      auto pages_at = [&](int i) {
+        const int e = box0 + i + lane;
+        return e * box < job.kv && i < n * per ? row[e >> wide] : 0;
+      };
+      int pages = pages_at(0), pages_next = pages_at(32), pg = 0, before = 0;
+      auto load = [&](const CUtensorMap* tm, uint8_t* ring, uint64_t* full, uint64_t* empty, int i, int u, int page) {
+        const int slot = i % kSlots, pos = (job.u0 + u) * kStep;
+        if (i >= kSlots && !(good = __all_sync(0xffffffffu, mbar_wait(&empty[slot], (i / kSlots - 1) & 1, abort_p, kPWait)))) return;
+        const int boxes = min(per, (job.kv - pos + box - 1) / box);
+        if (lane == 0) mbar_expect_tx(&full[slot], boxes * box * HD * 2);
+        __syncwarp();
+        if (lane < boxes) {
+#pragma unroll
+          for (int h = 0; h < HD / 64; ++h)
+            tma_load_3d(ring + slot * Smem::kKv + h * (kStep * 128) + lane * box * 128, tm, h * 64, pos & (s.page - 1),
+                        page * s.kv + job.kvh, &full[slot]);
+        }
+      };
+      // K(0), K(1), V(0), K(2), V(1), ...: the order of the products
+      for (int u = 0; u <= n && good; ++u) {
+        before = pg;
+        if (u < n) {
+          const int at = u * per & 31;
+          if (at == 0 && u > 0) {
+            pages = pages_next;
+            pages_next = pages_at(u * per + 32);
+          }
+          pg = __shfl_sync(0xffffffffu, pages, (at + lane) & 31);
+          load(&tmK, ks, k_full, k_empty, kv_loads + u, u, pg);
           if (!good) break;
-          if (lane == 0) mbar_expect_tx(&full[slot], held * s.page * HD * 2);
-          __syncwarp();
-          loads = i + 1;
-          if (pg >= 0)
-            for (int h = 0; h < HD / 64; ++h)
-              tma_load_3d(ring + slot * kOperand + h * (kTile * 128) + lane * s.page * 128, kv ? &tmV : &tmK, h * 64, 0,
-                          pg * s.kv + kvh, &full[slot]);
+          k_loads = kv_loads + u + 1;
+        }
+        if (u > 0) {
+          load(&tmV, vs, v_full, v_empty, kv_loads + u - 1, u - 1, before);
+          if (!good) break;
+          v_loads = kv_loads + u;
         }
       }
+      kv_loads += n;
     }
   } else {
-    // ------------------------------------------------------------ V tiles with positions not every row attends
-    const int me = threadIdx.x - 320;
+    // ------------------------------------------------------------ V steps with positions not every row attends
     constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
-    // A full barrier's parity means something only to a waiter that knows the phase before has passed: for
-    // the uses before the first dirty tile the product warp, which waits for each, says so.
-    bool good = dirty_from == 0 || dirty_from >= n || mbar_wait(&near, 0, abort_p, kPWait);
-    for (int j = dirty_from; j < n && good; ++j) {
-      const int i = 2 * j + 1, slot = i % kSlots;
-      if (!(good = mbar_wait(&full[slot], (i / kSlots) & 1, abort_p, kPWait))) break;
-      uint8_t* tile = ring + slot * kOperand;
-      for (int e = me; e < kTile * HD / 8; e += 64) {
-        const int pos = j * kTile + ((e >> 3) & 127);
-        uint4* at = reinterpret_cast<uint4*>(tile + e * 16);  // [half][row][8 chunks]; a row's chunks stay in it
-        if (pos >= kv_len) {
-          *at = make_uint4(0, 0, 0, 0);
-        } else if (pos > shift + tok0) {
-          uint4 x = *at;
-          uint32_t w[4] = {x.x, x.y, x.z, x.w};
-          bool bad = false;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if ((w[k] & kExp) == kExp) bad = true, w[k] &= 0xffff0000u;
-            if (((w[k] >> 16) & kExp) == kExp) bad = true, w[k] &= 0x0000ffffu;
-          }
-          if (bad) {
-            *at = make_uint4(w[0], w[1], w[2], w[3]);
-            *(volatile int*)&dirty = 1;
+    bool good = true;
+    int vc = 0;
+    for (int nj = 0; good; ++nj) {
+      if (!(good = mbar_wait(&job_full[nj & 1], (nj >> 1) & 1, abort_p, kPWait))) break;
+      Job& job = jobs[nj & 1];
+      if (job.lane < 0) break;
+      const int every = job.kv - job.n_q + job.tok0;  // the last position that every row attends
+      for (int u = job.dirty_from; u < job.n && good; ++u) {
+        const int i = vc + u, slot = i % kSlots;
+        // a barrier's parity means something only to a waiter that knows the phase before has passed: the
+        // product warp of tile 0, which waits for every load, says which it has seen
+        const long long t0 = clock64();
+        while (*(volatile int*)&v_seen < i - kSlots + 1 && good) {
+          __nanosleep(100);
+          if (*abort_p || clock64() - t0 > kPWait) {
+            *abort_p = 1;
+            good = false;
           }
         }
+        if (!good || !(good = mbar_wait(&v_full[slot], (i / kSlots) & 1, abort_p, kPWait))) break;
+        uint8_t* tile = vs + slot * Smem::kKv;
+        for (int e = lane; e < kStep * HD / 8; e += 32) {
+          const int pos = (job.u0 + u) * kStep + ((e >> 3) & (kStep - 1));
+          uint4* at = reinterpret_cast<uint4*>(tile + e * 16);  // [half][row][8 chunks]; a row's chunks stay in it
+          if (pos >= job.kv) {
+            *at = make_uint4(0, 0, 0, 0);
+          } else if (pos > every) {
+            uint4 x = *at;
+            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            bool bad = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if ((w[k] & kExp) == kExp) bad = true, w[k] &= 0xffff0000u;
+              if (((w[k] >> 16) & kExp) == kExp) bad = true, w[k] &= 0x0000ffffu;
+            }
+            if (bad) {
+              *at = make_uint4(w[0], w[1], w[2], w[3]);
+              *(volatile int*)&job.dirty = 1;
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&v_clean[slot]);
       }
-      fence_proxy_async_smem();
-      mbar_arrive(&clean[j % kVSlots]);  // one barrier a slot: the cleaning may run ahead of the products
+      vc += job.n;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&job_empty[nj & 1]);
     }
-  }
   }
 
   __syncthreads();
@@ -502,20 +721,28 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // memory when the CTA exits (bounded waits)
     if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
     const long long t0 = clock64();
-    if (warp == 8 && issued) {
-      if (elect_one()) mma_commit(&fin);
+    if ((warp == 8 || warp == 11) && issued) {
+      if (elect_one()) mma_commit(&fin[warp == 11]);
       __syncwarp();
-      while (!mbar_try_wait(&fin, 0) && clock64() - t0 < kPWait) {
+      while (!mbar_try_wait(&fin[warp == 11], 0) && clock64() - t0 < kPWait) {
       }
     }
-    if (warp == 9 && n > 0) {
-      while (!mbar_try_wait(&q_full, 0) && clock64() - t0 < kPWait) {
+    if (warp == 9) {
+      while (q_loads > 0 && !mbar_try_wait(&q_full, (q_loads - 1) & 1) && clock64() - t0 < kPWait) {
       }
-      for (int i = max(0, loads - kSlots); i < loads; ++i)
-        while (!mbar_try_wait(&full[i % kSlots], (i / kSlots) & 1) && clock64() - t0 < kPWait) {
+      for (int i = max(0, k_loads - kSlots); i < k_loads; ++i)
+        while (!mbar_try_wait(&k_full[i % kSlots], (i / kSlots) & 1) && clock64() - t0 < kPWait) {
+        }
+      for (int i = max(0, v_loads - kSlots); i < v_loads; ++i)
+        while (!mbar_try_wait(&v_full[i % kSlots], (i / kSlots) & 1) && clock64() - t0 < kPWait) {
         }
     }
     __syncthreads();
+  }
+  if (threadIdx.x == 288 && atomicAdd(p.queue + 1, 1) == (int)gridDim.x - 1) {
+    // the last CTA leaves the queue as the next call needs it
+    p.queue[0] = 0;
+    p.queue[1] = 0;
   }
   if (warp == 8) {
     tc_fence_after();
@@ -550,19 +777,17 @@ bool make_tmap3(CUtensorMap* tm, const void* base, bool bf16, uint64_t x, uint64
 
 template <int HD, bool BF16>
 cudaError_t launch_as(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, const PromptParams& p,
-                      cudaStream_t st) {
+                      long long blocks, cudaStream_t st) {
   int limit = 0;
   cudaError_t e = dyn_smem_limit((const void*)paged_prompt_kernel<HD, BF16>, &limit);
   if (e != cudaSuccess) return e;
   if (PromptSmem<HD>::kBytes > limit) return cudaErrorInvalidConfiguration;
-  const int tq = kTile / p.pack;
-  const long long blocks = (long long)p.n_rows / (2 * tq) + p.n_lanes;  // at least the lanes' blocks
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = st;
-  cfg.gridDim = dim3((unsigned)(blocks * (p.n_heads / p.pack)));
+  cfg.gridDim = dim3((unsigned)min((long long)kSms, blocks * p.pieces));
   cfg.blockDim = dim3(kPromptThreads);
   cfg.dynamicSmemBytes = PromptSmem<HD>::kBytes;
   profile_stream_begin(st);
@@ -578,19 +803,36 @@ cudaError_t launch_paged_prompt(const PagedPromptArgs& a, cudaStream_t st) {
   const PagedShape& s = a.s;
   const size_t off = (size_t)a.layer * s.layer_elems();
   const int group = a.n_heads / s.kv;
-  int pack = group & -group;  // largest power of two that divides the group
-  if (pack > kTile) pack = kTile;
+  const int pack = prompt_pack(s, a.n_heads);
   const bool bf16 = s.dtype == TL_KV_BF16;
   alignas(64) CUtensorMap tmQ, tmK, tmV;
-  const uint64_t blocks = (uint64_t)s.n_pages * s.kv;
+  const uint64_t rows = (uint64_t)s.n_pages * s.kv;
+  const uint32_t box = s.page < kStep ? s.page : kStep;
   if (!make_tmap3(&tmQ, a.q, bf16, s.hd, a.n_heads, a.n_rows, s.hd * 2, (uint64_t)a.q_stride * 2, pack, kTile / pack) ||
-      !make_tmap3(&tmK, a.c.k + off, bf16, s.hd, s.page, blocks, s.hd * 2, s.block_elems() * 2, s.page, 1) ||
-      !make_tmap3(&tmV, a.c.v + off, bf16, s.hd, s.page, blocks, s.hd * 2, s.block_elems() * 2, s.page, 1))
+      !make_tmap3(&tmK, a.c.k + off, bf16, s.hd, s.page, rows, s.hd * 2, s.block_elems() * 2, box, 1) ||
+      !make_tmap3(&tmV, a.c.v + off, bf16, s.hd, s.page, rows, s.hd * 2, s.block_elems() * 2, box, 1))
     return cudaErrorInvalidValue;
-  const PromptParams p{s,      a.c.v + off, a.c.table,           a.cu_q,         a.kv_len, a.seqs,
-                       (uint16_t*)a.out, (uint32_t*)a.ws, a.scale * kLog2e, a.n_heads, group, pack, a.n_rows, a.n_lanes};
-  if (s.hd == 64) return bf16 ? launch_as<64, true>(tmQ, tmK, tmV, p, st) : launch_as<64, false>(tmQ, tmK, tmV, p, st);
-  return bf16 ? launch_as<128, true>(tmQ, tmK, tmV, p, st) : launch_as<128, false>(tmQ, tmK, tmV, p, st);
+  const PromptParams p{s,
+                       a.c.v + off,
+                       a.c.table,
+                       a.cu_q,
+                       a.kv_len,
+                       a.seqs,
+                       (uint16_t*)a.out,
+                       (uint32_t*)a.ws,
+                       (int32_t*)(a.ws + kPagedQueueOff),
+                       (int32_t*)(a.ws + 256),
+                       (float*)(a.ws + kPagedHead),
+                       a.scale * kLog2e,
+                       a.n_heads,
+                       group,
+                       pack,
+                       a.n_rows,
+                       a.n_lanes,
+                       a.plan.pieces};
+  if (s.hd == 64)
+    return bf16 ? launch_as<64, true>(tmQ, tmK, tmV, p, a.plan.blocks, st) : launch_as<64, false>(tmQ, tmK, tmV, p, a.plan.blocks, st);
+  return bf16 ? launch_as<128, true>(tmQ, tmK, tmV, p, a.plan.blocks, st) : launch_as<128, false>(tmQ, tmK, tmV, p, a.plan.blocks, st);
 }
 
 }  // namespace tl

@@ -43,8 +43,11 @@ __host__ __device__ inline int paged_splits(int len, int target, int fixed) {
   return len <= rows ? 1 : (len + rows - 1) / rows;
 }
 
-// Workspace: status word | per-split (max, sum) and unnormalised sums of the decode; the plan of the
-// operations on pages (counters | moves: source, destination | one word per page) lies over them.
+// Workspace: a head that is zero between calls (status word | work queue of the prompt attention |
+// finished pieces of its blocks), then, one over the other: per-split (max, sum) and unnormalised sums
+// of the decode; partial results of the prompt attention; the plan of the operations on pages (counters |
+// moves: source, destination | one word per page).
+constexpr int kPagedQueueOff = 128, kPagedHead = 4096;
 struct PagedWorkspace {
   size_t ml_off, acc_off, total;  // decode
   int s_max, target;              // splits a lane can have; paged_split_rows' target
@@ -61,7 +64,7 @@ inline PagedWorkspace paged_workspace(const PagedShape& s, int n_heads, int n_la
   if (w.s_max < coarse) w.s_max = coarse;
   if (split_rows) w.s_max = (len + split_rows - 1) / split_rows;
   const size_t parts = (size_t)n_lanes * n_heads * w.s_max;
-  w.ml_off = 256;
+  w.ml_off = kPagedHead;
   w.acc_off = align256(w.ml_off + parts * 8);
   w.total = align256(w.acc_off + parts * s.hd * 4);
   return w;
@@ -75,15 +78,42 @@ inline size_t paged_workspace_upto(const PagedShape& s, int n_heads, int n_lanes
   if (lane_splits < n_lanes * coarse) lane_splits = n_lanes * coarse;
   if (split_rows) lane_splits = n_lanes * (size_t)((s.max_len() + split_rows - 1) / split_rows);
   const size_t parts = lane_splits * n_heads;
-  return align256(align256(256 + parts * 8) + parts * s.hd * 4);
+  return align256(align256(kPagedHead + parts * 8) + parts * s.hd * 4);
+}
+// Prompt attention: heads packed into a tile's rows (the largest power of two up to 128 that divides the
+// group), blocks of two tiles there can be, and the pieces that a block may be cut into so that the SMs
+// have three each (a piece has at least kPieceSteps steps of 64 positions).
+constexpr int kPromptPieces = 444, kPromptMostPieces = 8, kPieceSteps = 8;
+static_assert(256 + kPromptPieces * 8 <= kPagedHead, "the counts of finished pieces lie in the head");
+inline int prompt_pack(const PagedShape& s, int n_heads) {
+  const int group = n_heads / s.kv, pack = group & -group;
+  return pack < 128 ? pack : 128;
+}
+struct PromptPlan {
+  long long blocks;
+  int pieces;
+  size_t total;
+};
+inline PromptPlan prompt_plan(const PagedShape& s, int n_heads, int n_lanes, int n_rows) {
+  const int pack = prompt_pack(s, n_heads);
+  PromptPlan w;
+  w.blocks = ((long long)n_rows / (256 / pack) + n_lanes) * (n_heads / pack);  // at least the lanes' blocks
+  const long long by_len = s.max_len() / (kPieceSteps * 64), by_sms = kPromptPieces / w.blocks;
+  w.pieces = (int)(by_len < by_sms ? by_len : by_sms);
+  w.pieces = w.pieces < 1 ? 1 : w.pieces > kPromptMostPieces ? kPromptMostPieces : w.pieces;
+  w.total = kPagedHead + (w.pieces > 1 ? (size_t)w.blocks * w.pieces * 2 * 128 * (s.hd + 2) * 4 : 0);
+  return w;
+}
+inline size_t prompt_workspace_most(const PagedShape& s) {
+  return kPagedHead + (s.max_len() >= 2 * kPieceSteps * 64 ? (size_t)kPromptPieces * 2 * 128 * (s.hd + 2) * 4 : 0);
 }
 struct PagedOpsWorkspace {
   size_t count_off, moves_off, list_off, total;
 };
 inline PagedOpsWorkspace paged_ops_workspace(const PagedShape& s) {
   PagedOpsWorkspace w;
-  w.count_off = 256;
-  w.moves_off = 512;
+  w.count_off = kPagedHead;
+  w.moves_off = kPagedHead + 256;
   w.list_off = align256(w.moves_off + (size_t)s.n_pages * 8);
   w.total = align256(w.list_off + (size_t)s.n_pages * 4);
   return w;
@@ -114,6 +144,7 @@ struct PagedPromptArgs {
   float scale;
   void* out;
   uint8_t* ws;
+  PromptPlan plan;
 };
 
 cudaError_t launch_paged_append(const PagedShape& s, const PagedBufs& c, int layer, const void* k_rows, int64_t k_stride,

@@ -1,6 +1,8 @@
 // C ABI of the paged K/V cache (include/tl_paged.h): host-side validation and kernel launches.
 #include <math.h>
 
+#include <initializer_list>
+
 #include "paged_internal.cuh"
 
 namespace {
@@ -136,8 +138,10 @@ tl_status tl_paged_workspace_bytes(const tl_paged_desc* desc, int32_t n_heads, i
   if (n_lanes > tl::kPagedMaxLanes)
     return set_error(TL_ERR_UNSUPPORTED, "n_lanes %d > %d lanes per call", n_lanes, tl::kPagedMaxLanes);
   if ((st = check_split(split_rows)) != TL_OK) return st;
-  const size_t decode = tl::paged_workspace_upto(s, n_heads, n_lanes, split_rows), ops = tl::paged_ops_workspace(s).total;
-  *bytes = decode > ops ? decode : ops;
+  size_t most = tl::paged_workspace_upto(s, n_heads, n_lanes, split_rows);
+  for (const size_t need : {tl::paged_ops_workspace(s).total, tl::prompt_workspace_most(s)})
+    if (need > most) most = need;
+  *bytes = most;
   return TL_OK;
 }
 
@@ -212,10 +216,13 @@ tl_status tl_paged_prompt_attn(const tl_paged_desc* desc, tl_paged_cache cache, 
   if (n_rows > (1 << 24)) return set_error(TL_ERR_UNSUPPORTED, "n_rows %d > 2^24", n_rows);
   if ((st = check_stride(&q_stride, (int64_t)n_heads * s.hd, "q_stride")) != TL_OK) return st;
   if ((st = check_scale(&scale, s.hd)) != TL_OK) return st;
-  if ((st = check_workspace(workspace, workspace_bytes, 256)) != TL_OK) return st;
+  const tl::PromptPlan plan = tl::prompt_plan(s, n_heads, n_lanes, n_rows);
+  if ((st = check_workspace(workspace, workspace_bytes, plan.total)) != TL_OK) return st;
+  if (plan.blocks > INT32_MAX / 4)
+    return set_error(TL_ERR_UNSUPPORTED, "%d rows of %d heads in one call", n_rows, n_heads);
   if (n_rows == 0) return TL_OK;
   const tl::PagedPromptArgs a{s, bufs(cache), layer, n_heads, n_lanes, n_rows, q, q_stride, cu_q,
-                              kv_len, seqs, scale, out, (uint8_t*)workspace};
+                              kv_len, seqs, scale, out, (uint8_t*)workspace, plan};
   cudaError_t e = tl::launch_paged_prompt(a, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_error(e, "tl_paged_prompt_attn launch");
   return TL_OK;

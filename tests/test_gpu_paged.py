@@ -247,6 +247,8 @@ def test_decode_offsets_past_32_bits(tl):
     (1, 1, 128, 16, BF16, [513], [0]),
     (2, 8, 64, 16, FP16, [40, 41, 39], [1000, 0, 88]),
     (1, 128, 64, 16, BF16, [3, 2], [0, 50]),              # one token a tile
+    (1, 4, 128, 64, FP16, [70, 5, 0, 200], [3000, 100, 9, 5000]),   # blocks cut into pieces, up to eight
+    (2, 1, 64, 128, BF16, [700], [900]),
 ])
 def test_prompt_matches_oracle(tl, kv, group, hd, page, dtype, lens, cached):
     total = [a + b for a, b in zip(lens, cached)]
@@ -288,18 +290,19 @@ def test_prompt_rows_that_attend_nothing(tl):
     rig.check_prompt(0, q, cu, out)
 
 
-@pytest.mark.parametrize("hd,page,dtype", [(128, 16, BF16), (64, 128, FP16)])
-def test_prompt_is_causal_whatever_later_positions_hold(tl, hd, page, dtype):
-    """NaN and infinities in K and V of later positions reach only the queries that attend them."""
+@pytest.mark.parametrize("hd,page,dtype,before", [(128, 16, BF16, 0), (64, 128, FP16, 0), (128, 32, FP16, 2500)])
+def test_prompt_is_causal_whatever_later_positions_hold(tl, hd, page, dtype, before):
+    """NaN and infinities in K and V of later positions reach only the queries that attend them; with positions
+    cached before, in blocks that are cut into pieces too."""
     n, at = 390, 301
-    rig = Rig(tl, [n], kv=1, group=2, hd=hd, page=page, dtype=dtype, layers=1)
+    rig = Rig(tl, [n + before], kv=1, group=2, hd=hd, page=page, dtype=dtype, layers=1)
     q = rig.queries(n)
     out, clean = torch.empty_like(q), torch.empty_like(q)
-    tl.paged_prompt_attn(rig.cache, 0, q, _i32([0, n]), _i32([n]), clean)
-    slot = lambda pos: (0, int(rig.table[0, pos // page]), 0, pos % page)  # noqa: E731
+    tl.paged_prompt_attn(rig.cache, 0, q, _i32([0, n]), _i32([n + before]), clean)
+    slot = lambda i: (0, int(rig.table[0, (before + i) // page]), 0, (before + i) % page)  # noqa: E731
     rig.cache.v[slot(at)][3] = float("inf")
     rig.cache.v[slot(at + 20)][5] = float("nan")
-    tl.paged_prompt_attn(rig.cache, 0, q, _i32([0, n]), _i32([n]), out)
+    tl.paged_prompt_attn(rig.cache, 0, q, _i32([0, n]), _i32([n + before]), out)
     rig.ok()
     assert torch.equal(out[:at], clean[:at])
     assert torch.isinf(out[at:, :, 3]).all() and (out[at:, :, 3] > 0).all()
@@ -307,7 +310,7 @@ def test_prompt_is_causal_whatever_later_positions_hold(tl, hd, page, dtype):
     rest = [d for d in range(hd) if d not in (3, 5)]
     assert torch.equal(out[..., rest], clean[..., rest])
     rig.cache.k[slot(at)] = float("nan")
-    tl.paged_prompt_attn(rig.cache, 0, q, _i32([0, n]), _i32([n]), out)
+    tl.paged_prompt_attn(rig.cache, 0, q, _i32([0, n]), _i32([n + before]), out)
     assert torch.equal(out[:at], clean[:at]) and torch.isnan(out[at:]).all()
 
 
