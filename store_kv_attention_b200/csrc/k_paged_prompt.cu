@@ -20,12 +20,13 @@
 //             when there is nothing to wait for, pass behind the products of the other).  Each tile has
 //             two S buffers of 64 columns: S_t(u+2) is issued behind P_t(u) V(u), so that the next S
 //             is there while a tile's softmax runs and the tensor pipe has products meanwhile
-//   9         takes work and loads by TMA: Q once, K and V through two rings, page by page (a page of
-//             one K/V head is one box per 64 values)
-//   10        cleans the V steps that hold positions not every row attends: rows past the cache's end
-//             are zeroed (their memory may hold anything) and values that are not finite are taken
-//             out (0 x inf would reach the rows that do not attend them) and given back at the end
-//             to the rows that do
+//   9, 10     take work and load by TMA, page by page (a page of one K/V head is one box per 64 values):
+//             Q and K / V.  A slot of the ring holds what one issue of products takes, K(u+2) and V(u).
+//             (Two warps: a box costs some 50 clocks of issue, a step of 16-position pages 16 boxes.)
+//             Warp 9 also cleans the V steps that hold positions not every row attends, before it
+//             takes the next work: rows past the cache's end are zeroed (their memory may hold
+//             anything) and values that are not finite are taken out (0 x inf would reach the rows that
+//             do not attend them) and given back at the end to the rows that do
 // O is rescaled only when a row's maximum has grown by more than 2^8 in the exponent since the last
 // time: the base of the exponents is a free choice (P then reaches 2^8 and its sum 2^8 times the
 // positions, far inside FP32), and the rescale, a round trip of O through registers, becomes rare.
@@ -164,10 +165,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   // A wait by parity cannot tell a phase from the second one behind it, so every barrier is waited for in
   // each of its phases in turn, or its next phase needs the waiter; what may be two steps behind has two.
-  __shared__ uint64_t q_full, q_empty, k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots], v_clean[kSlots];
+  __shared__ uint64_t q_full, q_empty, full[kSlots], empty[kSlots], clean[kSlots];
   __shared__ uint64_t s_full[2][2], p_full[2][2], o_done[2][2], job_full[2], job_empty[2], part_done[2], part_said[2], fin[2];
   __shared__ uint32_t tmem_base;
-  __shared__ int abort_flag, v_seen, last_piece[2];
+  __shared__ int abort_flag, last_piece[2];
   __shared__ Job jobs[2];
   __shared__ int first_block[kPagedMaxLanes + 1];  // of each lane
   uint8_t* qs = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);  // two tiles
@@ -181,11 +182,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     mbar_init(&q_full, 1);
     mbar_init(&q_empty, 2);
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 2);  // both tiles
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 2);
-      mbar_init(&v_clean[i], 32);
+      mbar_init(&full[i], 2);   // K's and V's loads
+      mbar_init(&empty[i], 2);  // both tiles
+      mbar_init(&clean[i], 32);
     }
     for (int t = 0; t < 2; ++t) {
       for (int i = 0; i < 2; ++i) {
@@ -200,7 +199,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&job_empty[t], 11);  // warps that read a job
     }
     abort_flag = 0;
-    v_seen = 0;
     mbar_fence_init();
   }
   pdl_wait();
@@ -215,7 +213,45 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   volatile int* abort_p = &abort_flag;
   pdl_trigger();  // TMEM is held
   bool issued = false;                 // products issued (warps 8, 11)
-  int q_loads = 0, k_loads = 0, v_loads = 0;  // (warp 9)
+  int q_loads = 0, loads = 0;          // jobs and slots loaded (warps 9, 10)
+
+  // Loads a job's steps of K (behind 0) or V (behind 2) into ring: step u into slot loads + u + behind.
+  const int box = min(s.page, kStep), per = kStep / box;  // rows of a TMA box, boxes of a step
+  const int wide = s.page / box - 1;                      // 1: a page is two boxes (128 positions)
+  auto load_steps = [&](const Job& job, const CUtensorMap* tm, uint8_t* ring, int behind, auto before) {
+    const int32_t* row = p.table + (size_t)job.seq * s.max_pages;
+    // pages of 32 boxes at a time, one per lane, and of the 32 behind them
+    auto pages_at = [&](int i) {
+      const int e = job.u0 * per + i + lane;
+      return e * box < job.kv && i < job.n * per ? row[e >> wide] : 0;
+    };
+    int pages = pages_at(0), pages_next = pages_at(32);
+    for (int w = 0; w < job.n + 2; ++w, ++loads) {
+      const int slot = loads % kSlots, u = w - behind, pos = (job.u0 + u) * kStep;
+      if (!before(w)) return false;
+      if (loads >= kSlots && !__all_sync(0xffffffffu, mbar_wait(&empty[slot], (loads / kSlots - 1) & 1, abort_p, kPWait))) return false;
+      if (u < 0 || u >= job.n) {
+        if (lane == 0) mbar_arrive(&full[slot]);
+        continue;
+      }
+      const int at = u * per & 31;
+      if (at == 0 && u > 0) {
+        pages = pages_next;
+        pages_next = pages_at(u * per + 32);
+      }
+      const int page = __shfl_sync(0xffffffffu, pages, (at + lane) & 31);
+      const int boxes = min(per, (job.kv - pos + box - 1) / box);
+      if (lane == 0) mbar_expect_tx(&full[slot], boxes * box * HD * 2);
+      if (lane < boxes) {
+#pragma unroll
+        for (int h = 0; h < HD / 64; ++h)
+          tma_load_3d(ring + slot * Smem::kKv + h * (kStep * 128) + lane * box * 128, tm, h * 64, pos & (s.page - 1),
+                      page * s.kv + job.kvh, &full[slot]);
+      }
+      __syncwarp();
+    }
+    return true;
+  };
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax of tile t, row r
@@ -427,8 +463,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const uint64_t q_desc = sdesc_sw128(smem_addr(qs + t * Smem::kQ), 16, 1024);
     const uint64_t k_desc = sdesc_sw128(smem_addr(ks), 16, 1024), v_desc = sdesc_sw128(smem_addr(vs), kStep * 128, 1024);
     const uint32_t ts = tbase + t * 128, to = tbase + 256 + t * HD;
-    int kv = 0, c = 0;         // steps of K and V, and of this tile, before this job
-    uint32_t clean_phase = 0;  // one bit per V slot
+    int at = 0, c = 0;         // slots, and steps of this tile, before this job
+    uint32_t clean_phase = 0;  // one bit per slot
     for (int nj = 0; good; ++nj) {
       if (!wait(&job_full[nj & 1], (nj >> 1) & 1)) break;
       const Job& job = jobs[nj & 1];
@@ -436,67 +472,53 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int n = job.n, nt = job.n_t[t], dirty_from = job.dirty_from;
       __syncwarp();
       if (lane == 0) mbar_arrive(&job_empty[nj & 1]);
-      auto scores = [&](int u) {  // S_t(u) = Q_t K(u)^T
-        const int slot = (kv + u) % kSlots, buf = (c + u) & 1;
-        const uint64_t b = k_desc + (uint64_t)((slot * Smem::kKv) >> 4);
-#pragma unroll
-        for (int k = 0; k < HD / 16; ++k)
-          mma_ss(ts + buf * kStep, q_desc + (uint64_t)(((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4),
-                 b + (uint64_t)(((k / 4) * (kStep * 128) + (k % 4) * 32) >> 4), kIdS, k != 0);
-        mma_commit(&s_full[t][buf]);
-        mma_commit(&k_empty[slot]);
-        if (u == n - 1) mma_commit(&q_empty);
-      };
-      auto product = [&](int u) {  // O_t += P_t(u) V(u)
-        const int slot = (kv + u) % kSlots, buf = (c + u) & 1;
-        const uint64_t b = v_desc + (uint64_t)((slot * Smem::kKv) >> 4);
-#pragma unroll
-        for (int k = 0; k < kStep / 16; ++k)
-          mma_ts(to, ts + buf * kStep + k * 8, b + (uint64_t)((k * 2048) >> 4), kIdO, (u | k) != 0);
-        mma_commit(&o_done[t][buf]);
-        mma_commit(&v_empty[slot]);
-      };
-      // steps that this tile does not attend: their slots (and the queries) are given back unread
-      auto pass_k = [&](int u) {
-        if (lane == 0) {
-          mbar_arrive(&k_empty[(kv + u) % kSlots]);
-          if (u == n - 1) mbar_arrive(&q_empty);
+      if (n == 0) continue;
+      if (!wait(&q_full, nj & 1)) break;
+      // turn w: O_t += P_t(w - 2) V(w - 2), then S_t(w) = Q_t K(w)^T; both operands lie in slot at + w
+      for (int w = 0; w < n + 2; ++w) {
+        const int slot = (at + w) % kSlots, u = w - 2;
+        if (!wait(&full[slot], ((at + w) / kSlots) & 1)) break;
+        if (u >= dirty_from && u >= 0) {
+          if (!wait(&clean[slot], (clean_phase >> slot) & 1)) break;
+          clean_phase ^= 1u << slot;
         }
-      };
-      if (n > 0 && !wait(&q_full, nj & 1)) break;
-      for (int u = 0; u < 2 && u < n; ++u) {
-        if (!wait(&k_full[(kv + u) % kSlots], ((kv + u) / kSlots) & 1)) break;
+        const bool pv = u >= 0 && u < nt, qk = w < nt;
+        const int buf = (c + w) & 1;  // of step w and of step u
+        if (pv && !wait(&p_full[t][buf], ((c + u) >> 1) & 1)) break;
         tc_fence_after();
-        if (u >= nt)
-          pass_k(u);
-        else if (elect_one())
-          scores(u);
+        if (elect_one()) {
+          if (pv) {
+            const uint64_t b = v_desc + (uint64_t)((slot * Smem::kKv) >> 4);
+#pragma unroll
+            for (int k = 0; k < kStep / 16; ++k)
+              mma_ts(to, ts + buf * kStep + k * 8, b + (uint64_t)((k * 2048) >> 4), kIdO, (u | k) != 0);
+            mma_commit(&o_done[t][buf]);
+          }
+          if (qk) {
+            const uint64_t b = k_desc + (uint64_t)((slot * Smem::kKv) >> 4);
+#pragma unroll
+            for (int k = 0; k < HD / 16; ++k)
+              mma_ss(ts + buf * kStep, q_desc + (uint64_t)(((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4),
+                     b + (uint64_t)(((k / 4) * (kStep * 128) + (k % 4) * 32) >> 4), kIdS, k != 0);
+            mma_commit(&s_full[t][buf]);
+          }
+          // the slot (after the last scores the queries too) is free once these products are done; at once
+          // where this tile attends neither
+          if (pv || qk)
+            mma_commit(&empty[slot]);
+          else
+            mbar_arrive(&empty[slot]);
+          if (w == n - 1) {
+            if (qk)
+              mma_commit(&q_empty);
+            else
+              mbar_arrive(&q_empty);
+          }
+        }
         __syncwarp();
         issued = true;
       }
-      for (int u = 0; u < n && good; ++u) {
-        const int slot = (kv + u) % kSlots;
-        if (!wait(&v_full[slot], ((kv + u) / kSlots) & 1)) break;
-        if (t == 0 && lane == 0) *(volatile int*)&v_seen = kv + u + 1;
-        if (u >= dirty_from) {
-          if (!wait(&v_clean[slot], (clean_phase >> slot) & 1)) break;
-          clean_phase ^= 1u << slot;
-        }
-        if (u + 2 < n && !wait(&k_full[(kv + u + 2) % kSlots], ((kv + u + 2) / kSlots) & 1)) break;
-        if (u < nt) {
-          if (!wait(&p_full[t][(c + u) & 1], ((c + u) >> 1) & 1)) break;
-          tc_fence_after();
-          if (elect_one()) {
-            product(u);
-            if (u + 2 < nt) scores(u + 2);
-          }
-        } else if (lane == 0) {
-          mbar_arrive(&v_empty[slot]);
-        }
-        if (u + 2 < n && u + 2 >= nt) pass_k(u + 2);
-        __syncwarp();
-      }
-      kv += n;
+      at += n + 2;
       c += nt;
     }
   } else if (warp == 9) {
@@ -526,168 +548,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     if (lane == 0) first_block[p.n_lanes] = blocks;
     __syncwarp();
     const int items = blocks * subs * p.pieces;
-    const int box = min(s.page, kStep), per = kStep / box;  // rows of a TMA box, boxes of a step
-    const int wide = s.page / box - 1;                      // 1: a page is two boxes (128 positions)
-    bool good = true;
-    int taken = blockIdx.x, kv_loads = 0;
-    for (int nj = 0; good;) {
-      const int item = taken;
-      if (item < items) {
-        int next = 0;
-        if (lane == 0) next = gridDim.x + atomicAdd(p.queue, 1);
-        taken = __shfl_sync(0xffffffffu, next, 0);
-      }
-      Job job = {};
-      job.lane = -1;
-      const int32_t* row = nullptr;
-      if (item < items) {
-        const int piece = item % p.pieces, bs = item / p.pieces, sub = bs % subs, blk = bs / subs;
-        int lo = 0, hi = p.n_lanes;
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (first_block[mid] <= blk)
-            lo = mid;
-          else
-            hi = mid;
-        }
-        job.lane = lo;
-        job.q0 = p.cu_q[lo];
-        job.n_q = p.cu_q[lo + 1] - job.q0;
-        job.kv = p.kv_len[lo];
-        job.seq = p.seqs ? p.seqs[lo] : lo;
-        bool ok = job.seq >= 0 && job.seq < s.max_seqs && job.kv >= 0 && job.kv <= s.max_len();
-        if (ok) {
-          // every position of the lane has to have a page of the pool
-          row = p.table + (size_t)job.seq * s.max_pages;
-          const int held = (job.kv + s.page - 1) / s.page;
-#pragma unroll 4
-          for (int j = lane; j < held; j += 32) {
-            const int pg = row[j];
-            ok = ok && pg >= 0 && pg < s.n_pages;
-          }
-        }
-        if (!__all_sync(0xffffffffu, ok)) {
-          if (lane == 0) atomicOr(p.status, kStatusRange);
-          continue;
-        }
-        job.tok0 = (first_block[lo + 1] - 1 - blk) * 2 * tq;  // a lane's last block first
-        job.head0 = sub * p.pack;
-        job.kvh = job.head0 / p.group;
-        const int shift = job.kv - job.n_q;
-        int n_t[2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          // steps a tile needs, by its last token's position
-          const int first = job.tok0 + t * tq, last = shift + min(job.n_q, first + tq) - 1;
-          n_t[t] = first < job.n_q && last >= 0 ? last / kStep + 1 : 0;
-        }
-        const int all = max(n_t[0], n_t[1]);
-        job.pieces = max(1, min(p.pieces, all / kPieceSteps));
-        const int each = (all + job.pieces - 1) / job.pieces;
-        if (piece >= job.pieces) continue;
-        job.piece = piece;
-        job.slot = bs * p.pieces;
-        job.u0 = piece * each;
-        job.n = max(0, min(each, all - job.u0));
-        for (int t = 0; t < 2; ++t) job.n_t[t] = max(0, min(job.n, n_t[t] - job.u0));
-        job.dirty_from = max(0, max(0, shift + job.tok0 + 1) / kStep - job.u0);
-      }
-      if (nj >= 2) good = __all_sync(0xffffffffu, mbar_wait(&job_empty[nj & 1], ((nj >> 1) - 1) & 1, abort_p, kPWait));
-      if (!good) break;
-      if (lane == 0) {
-        jobs[nj & 1] = job;
-        mbar_arrive(&job_full[nj & 1]);
-      }
-      __syncwarp();
-      if (job.lane < 0) break;
-      const int n = job.n;
-      if (n == 0) {
-        // q_full's and q_empty's phases go by jobs: an empty one passes its turn on
-        if (nj > 0 && !(good = __all_sync(0xffffffffu, mbar_wait(&q_empty, (nj - 1) & 1, abort_p, kPWait)))) break;
-        if (lane == 0) {
-          mbar_arrive(&q_full);
-          mbar_arrive(&q_empty);
-          mbar_arrive(&q_empty);
-        }
-        ++nj;
-        continue;
-      }
-      if (nj > 0 && !(good = __all_sync(0xffffffffu, mbar_wait(&q_empty, (nj - 1) & 1, abort_p, kPWait)))) break;
-      if (lane == 0) {
-        mbar_expect_tx(&q_full, 2 * Smem::kQ);
-        for (int t = 0; t < 2; ++t)
-          for (int h = 0; h < HD / 64; ++h)
-            tma_load_3d(qs + t * Smem::kQ + h * (kTile * 128), &tmQ, h * 64, job.head0, job.q0 + job.tok0 + t * tq, &q_full);
-      }
-      q_loads = ++nj;
-      // pages of 32 boxes at a time, one per lane, and of the 32 behind them
-      const int box0 = job.u0 * per;
-      auto pages_at = [&](int i) {
-        const int e = box0 + i + lane;
-        return e * box < job.kv && i < n * per ? row[e >> wide] : 0;
-      };
-      int pages = pages_at(0), pages_next = pages_at(32), pg = 0, before = 0;
-      auto load = [&](const CUtensorMap* tm, uint8_t* ring, uint64_t* full, uint64_t* empty, int i, int u, int page) {
-        const int slot = i % kSlots, pos = (job.u0 + u) * kStep;
-        if (i >= kSlots && !(good = __all_sync(0xffffffffu, mbar_wait(&empty[slot], (i / kSlots - 1) & 1, abort_p, kPWait)))) return;
-        const int boxes = min(per, (job.kv - pos + box - 1) / box);
-        if (lane == 0) mbar_expect_tx(&full[slot], boxes * box * HD * 2);
-        __syncwarp();
-        if (lane < boxes) {
-#pragma unroll
-          for (int h = 0; h < HD / 64; ++h)
-            tma_load_3d(ring + slot * Smem::kKv + h * (kStep * 128) + lane * box * 128, tm, h * 64, pos & (s.page - 1),
-                        page * s.kv + job.kvh, &full[slot]);
-        }
-      };
-      // K(0), K(1), V(0), K(2), V(1), ...: the order of the products
-      for (int u = 0; u <= n && good; ++u) {
-        before = pg;
-        if (u < n) {
-          const int at = u * per & 31;
-          if (at == 0 && u > 0) {
-            pages = pages_next;
-            pages_next = pages_at(u * per + 32);
-          }
-          pg = __shfl_sync(0xffffffffu, pages, (at + lane) & 31);
-          load(&tmK, ks, k_full, k_empty, kv_loads + u, u, pg);
-          if (!good) break;
-          k_loads = kv_loads + u + 1;
-        }
-        if (u > 0) {
-          load(&tmV, vs, v_full, v_empty, kv_loads + u - 1, u - 1, before);
-          if (!good) break;
-          v_loads = kv_loads + u;
-        }
-      }
-      kv_loads += n;
-    }
-  } else {
-    // ------------------------------------------------------------ V steps with positions not every row attends
+    // Cleans the next V steps of a job that need it, up to step `end`; `first` is the job's first slot.  (This
+    // warp waited for the slots to be free, so it knows which phase of their loads it waits for.)
     constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
-    bool good = true;
-    int vc = 0;
-    for (int nj = 0; good; ++nj) {
-      if (!(good = mbar_wait(&job_full[nj & 1], (nj >> 1) & 1, abort_p, kPWait))) break;
-      Job& job = jobs[nj & 1];
-      if (job.lane < 0) break;
+    int dirty_next = 0;
+    auto clean_steps = [&](Job& job, int first, int end) {
       const int every = job.kv - job.n_q + job.tok0;  // the last position that every row attends
-      for (int u = job.dirty_from; u < job.n && good; ++u) {
-        const int i = vc + u, slot = i % kSlots;
-        // a barrier's parity means something only to a waiter that knows the phase before has passed: the
-        // product warp of tile 0, which waits for every load, says which it has seen
-        const long long t0 = clock64();
-        while (*(volatile int*)&v_seen < i - kSlots + 1 && good) {
-          __nanosleep(100);
-          if (*abort_p || clock64() - t0 > kPWait) {
-            *abort_p = 1;
-            good = false;
-          }
-        }
-        if (!good || !(good = mbar_wait(&v_full[slot], (i / kSlots) & 1, abort_p, kPWait))) break;
+      for (; dirty_next < end; ++dirty_next) {
+        const int i = first + dirty_next + 2, slot = i % kSlots;
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], (i / kSlots) & 1, abort_p, kPWait))) return false;
         uint8_t* tile = vs + slot * Smem::kKv;
         for (int e = lane; e < kStep * HD / 8; e += 32) {
-          const int pos = (job.u0 + u) * kStep + ((e >> 3) & (kStep - 1));
+          const int pos = (job.u0 + dirty_next) * kStep + ((e >> 3) & (kStep - 1));
           uint4* at = reinterpret_cast<uint4*>(tile + e * 16);  // [half][row][8 chunks]; a row's chunks stay in it
           if (pos >= job.kv) {
             *at = make_uint4(0, 0, 0, 0);
@@ -707,11 +579,127 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
         }
         fence_proxy_async_smem();
-        mbar_arrive(&v_clean[slot]);
+        mbar_arrive(&clean[slot]);
       }
-      vc += job.n;
+      return true;
+    };
+    int item = blockIdx.x;
+    auto take = [&]() {  // the next job, or one with lane = -1
+      Job job = {};
+      job.lane = -1;
+      while (item < items) {
+        const int piece = item % p.pieces, bs = item / p.pieces, sub = bs % subs, blk = bs / subs;
+        int more = 0;
+        if (lane == 0) more = gridDim.x + atomicAdd(p.queue, 1);
+        item = __shfl_sync(0xffffffffu, more, 0);
+        int b = 0, hi = p.n_lanes;
+        while (hi - b > 1) {
+          const int mid = (b + hi) >> 1;
+          if (first_block[mid] <= blk)
+            b = mid;
+          else
+            hi = mid;
+        }
+        job.q0 = p.cu_q[b];
+        job.n_q = p.cu_q[b + 1] - job.q0;
+        job.kv = p.kv_len[b];
+        job.seq = p.seqs ? p.seqs[b] : b;
+        bool ok = job.seq >= 0 && job.seq < s.max_seqs && job.kv >= 0 && job.kv <= s.max_len();
+        if (ok) {
+          // every position of the lane has to have a page of the pool
+          const int32_t* row = p.table + (size_t)job.seq * s.max_pages;
+          const int held = (job.kv + s.page - 1) / s.page;
+#pragma unroll 4
+          for (int j = lane; j < held; j += 32) {
+            const int pg = row[j];
+            ok = ok && pg >= 0 && pg < s.n_pages;
+          }
+        }
+        if (!__all_sync(0xffffffffu, ok)) {
+          if (lane == 0) atomicOr(p.status, kStatusRange);
+          continue;
+        }
+        job.tok0 = (first_block[b + 1] - 1 - blk) * 2 * tq;  // a lane's last block first
+        job.head0 = sub * p.pack;
+        job.kvh = job.head0 / p.group;
+        const int shift = job.kv - job.n_q;
+        int n_t[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          // steps a tile needs, by its last token's position
+          const int first = job.tok0 + t * tq, last = shift + min(job.n_q, first + tq) - 1;
+          n_t[t] = first < job.n_q && last >= 0 ? last / kStep + 1 : 0;
+        }
+        const int all = max(n_t[0], n_t[1]);
+        job.pieces = max(1, min(p.pieces, all / kPieceSteps));
+        if (piece >= job.pieces) continue;
+        const int each = (all + job.pieces - 1) / job.pieces;
+        job.piece = piece;
+        job.slot = bs * p.pieces;
+        job.u0 = piece * each;
+        job.n = max(0, min(each, all - job.u0));
+        for (int t = 0; t < 2; ++t) job.n_t[t] = max(0, min(job.n, n_t[t] - job.u0));
+        job.dirty_from = max(0, max(0, shift + job.tok0 + 1) / kStep - job.u0);
+        job.lane = b;
+        break;
+      }
+      return job;
+    };
+    bool good = true;
+    Job next = take();
+    for (int nj = 0; good;) {
+      const Job job = next;
+      if (nj > 0) {  // what the job before has left, its last four slots
+        Job& last = jobs[(nj - 1) & 1];
+        good = clean_steps(last, loads - last.n - 2, last.n);
+      }
+      if (good && nj >= 2) good = __all_sync(0xffffffffu, mbar_wait(&job_empty[nj & 1], ((nj >> 1) - 1) & 1, abort_p, kPWait));
+      if (!good) break;
+      if (lane == 0) {
+        jobs[nj & 1] = job;
+        mbar_arrive(&job_full[nj & 1]);
+      }
+      __syncwarp();
+      if (job.lane < 0) break;
+      const int n = job.n;
+      if (n == 0) {
+        next = take();
+        // q_full's and q_empty's phases go by jobs: an empty one passes its turn on
+        if (nj > 0 && !(good = __all_sync(0xffffffffu, mbar_wait(&q_empty, (nj - 1) & 1, abort_p, kPWait)))) break;
+        if (lane == 0) {
+          mbar_arrive(&q_full);
+          mbar_arrive(&q_empty);
+          mbar_arrive(&q_empty);
+        }
+        ++nj;
+        continue;
+      }
+      if (nj > 0 && !(good = __all_sync(0xffffffffu, mbar_wait(&q_empty, (nj - 1) & 1, abort_p, kPWait)))) break;
+      if (lane == 0) {
+        mbar_expect_tx(&q_full, 2 * Smem::kQ);
+        for (int t = 0; t < 2; ++t)
+          for (int h = 0; h < HD / 64; ++h)
+            tma_load_3d(qs + t * Smem::kQ + h * (kTile * 128), &tmQ, h * 64, job.head0, job.q0 + job.tok0 + t * tq, &q_full);
+      }
+      q_loads = ++nj;
+      // the load of turn w waits for turn w - 4, which waits for its V step, w - 6, to be clean
+      dirty_next = job.dirty_from;
+      const int first = loads;
+      good = load_steps(job, &tmK, ks, 0, [&](int w) {
+        if (w == min(kSlots, n + 1)) next = take();  // while the ring is full
+        return clean_steps(jobs[(nj - 1) & 1], first, w - 5);
+      });
+    }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ loads of V
+    bool good = true;
+    for (int nj = 0; good; ++nj) {
+      if (!(good = __all_sync(0xffffffffu, mbar_wait(&job_full[nj & 1], (nj >> 1) & 1, abort_p, kPWait)))) break;
+      const Job job = jobs[nj & 1];
+      if (job.lane < 0) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&job_empty[nj & 1]);
+      if (job.n > 0) good = load_steps(job, &tmV, vs, 2, [](int) { return true; });
     }
   }
 
@@ -730,13 +718,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     if (warp == 9) {
       while (q_loads > 0 && !mbar_try_wait(&q_full, (q_loads - 1) & 1) && clock64() - t0 < kPWait) {
       }
-      for (int i = max(0, k_loads - kSlots); i < k_loads; ++i)
-        while (!mbar_try_wait(&k_full[i % kSlots], (i / kSlots) & 1) && clock64() - t0 < kPWait) {
-        }
-      for (int i = max(0, v_loads - kSlots); i < v_loads; ++i)
-        while (!mbar_try_wait(&v_full[i % kSlots], (i / kSlots) & 1) && clock64() - t0 < kPWait) {
-        }
     }
+    if (warp == 9 || warp == 10)
+      // a slot that only one of the two loaded does not fill: this wait then runs to its limit
+      for (int i = max(0, loads - kSlots); i < loads; ++i)
+        while (!mbar_try_wait(&full[i % kSlots], (i / kSlots) & 1) && clock64() - t0 < kPWait) {
+        }
     __syncthreads();
   }
   if (threadIdx.x == 288 && atomicAdd(p.queue + 1, 1) == (int)gridDim.x - 1) {
