@@ -75,7 +75,8 @@ struct PromptSmem {
   static constexpr int kQ = kTile * HD * 2;     // one tile of queries
   static constexpr int kKv = kStep * HD * 2;    // one step of K or of V
   static constexpr int kSlots = 4;              // of each ring
-  static constexpr int kBytes = 1024 + 2 * kQ + 2 * kSlots * kKv;
+  static constexpr int kStage = 8 * 32 * 64;    // of the outputs, a softmax warp's rows x 32 values
+  static constexpr int kBytes = 1024 + 2 * kQ + 2 * kSlots * kKv + kStage;
 };
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
@@ -154,21 +155,186 @@ struct Job {
   int dirty;    // a value that is not finite was taken out of V
 };
 
+// What the warps of a tile agree on when its block is cut into pieces.
+struct Joint {
+  uint64_t done[2], said[2];  // the piece's part is written; whether it is the last one is known
+  int last[2];
+};
+
+// The end of a tile's job, by the threads of its rows: O / l into the output, or the piece's part into the
+// workspace and, by the last piece, the parts joined.  (A function of its own, so that its registers are not
+// the softmax loop's.)  False: a wait gave up.
+template <int HD, bool BF16>
+__device__ __noinline__ bool finish_rows(const PromptParams& p, const Job& job, int t, uint32_t to, uint32_t stage,
+                                         float m, float l, Joint* joint, int& parts, volatile int* abort) {
+  constexpr int kPartFloats = kTile * (HD + 2);
+  const PagedShape& s = p.s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x & 127, log_pack = __ffs(p.pack) - 1;
+  const int tq = kTile >> log_pack, first = job.tok0 + t * tq, shift = job.kv - job.n_q;
+  const int tok = first + (r >> log_pack), lim = min(shift + tok, job.kv - 1);
+  const int nt = job.n_t[t], pos0 = job.u0 * kStep;
+  bool good = true;
+  const bool attends = nt > 0 && lim >= 0 && m != -INFINITY;
+  const bool store = tok < job.n_q;
+  const int fix0 = max(max(0, shift + job.tok0 + 1), pos0), fix1 = min(lim, pos0 + job.n * kStep - 1);
+  const bool fix = *(volatile const int*)&job.dirty != 0 && store;
+  const int32_t* row = p.table + (size_t)job.seq * s.max_pages;
+  // the values that were taken out of V, for the positions that this row attends
+  auto give_back = [&](int d, float* y) {
+    for (int pos = fix0; pos <= fix1; ++pos) {
+      const uint16_t* src = p.v + ((size_t)row[pos / s.page] * s.kv + job.kvh) * s.block_elems() + (size_t)(pos % s.page) * HD + d;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float v = unpack16<BF16>(src[i]);
+        if (!isfinite(v)) y[i] += v;
+      }
+    }
+  };
+  // 32 values of every row of the warp through shared memory, so that four lanes write 64 bytes of a row:
+  // this lane 16 bytes of rows lane / 4 + 0, 8, 16 and 24
+  uint16_t* dst[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = (warp & 3) * 32 + i * 8 + (lane >> 2), to_tok = first + (row >> log_pack);
+    dst[i] = to_tok < job.n_q ? p.out + ((size_t)(job.q0 + to_tok) * p.n_heads + job.head0 + (row & (p.pack - 1))) * HD + (lane & 3) * 8 : nullptr;
+  }
+  const uint32_t put_at = stage + lane * 64, get_at = stage + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+  auto put = [&](int d, const float* y) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(put_at + ((i ^ ((lane >> 1) & 3)) << 4)),
+                   "r"(pack16<BF16>(y[8 * i], y[8 * i + 1])), "r"(pack16<BF16>(y[8 * i + 2], y[8 * i + 3])),
+                   "r"(pack16<BF16>(y[8 * i + 4], y[8 * i + 5])), "r"(pack16<BF16>(y[8 * i + 6], y[8 * i + 7]))
+                   : "memory");
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint4 v;
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                   : "r"(get_at + i * 512)
+                   : "memory");
+      if (dst[i]) *reinterpret_cast<uint4*>(dst[i] + d) = v;
+    }
+    __syncwarp();
+  };
+  if (first >= job.n_q) {
+    // a tile without tokens
+  } else if (job.pieces == 1) {
+    const float inv = 1.0f / l;
+#pragma unroll 1
+    for (int d = 0; d < HD; d += 32) {
+      uint32_t o[32];
+      if (nt > 0) {  // warp-uniform
+        tmem_ld32(to + d, o);
+        tmem_ld_wait();
+      }
+      float y[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        asm volatile("" : "+r"(o[i]));
+        y[i] = attends ? __uint_as_float(o[i]) * inv : 0.0f;
+      }
+      if (fix) give_back(d, y);
+      put(d, y);
+    }
+  } else {
+    // leave the piece's part; the last piece of the tile to come by joins them all in their order
+    float* part = p.part + ((size_t)(job.slot + job.piece) * 2 + t) * kPartFloats;
+    reinterpret_cast<float2*>(part)[r] = make_float2(attends ? m : -INFINITY, l);
+    if (nt > 0) {
+#pragma unroll 1
+      for (int d = 0; d < HD; d += 32) {
+        uint32_t o[32];
+        tmem_ld32(to + d, o);
+        tmem_ld_wait();
+        float y[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          asm volatile("" : "+r"(o[i]));
+          y[i] = __uint_as_float(o[i]);
+        }
+        if (fix) give_back(d, y);
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+          reinterpret_cast<float4*>(part + 2 * kTile)[(d + i) / 4 * kTile + r] = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+      }
+    }
+    __threadfence();
+    mbar_arrive(&joint->done[t]);
+    if (r == 0 && (good = mbar_wait(&joint->done[t], parts & 1, abort, kPWait))) {
+      __threadfence();
+      int32_t* count = p.finished + job.slot * 2 + t;
+      const bool last = atomicAdd(count, 1) == job.pieces - 1;
+      if (last) *count = 0;
+      joint->last[t] = last;
+      mbar_arrive(&joint->said[t]);
+    }
+    good = __all_sync(0xffffffffu, good && mbar_wait(&joint->said[t], parts & 1, abort, kPWait));
+    if (!good) return false;
+    ++parts;
+    if (*(volatile int*)&joint->last[t]) {
+      __threadfence();
+      const float* base = p.part + ((size_t)job.slot * 2 + t) * kPartFloats;
+      const size_t next = 2 * kPartFloats;  // the following piece's
+      float f[kPromptMostPieces], top = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPromptMostPieces; ++i) {
+        f[i] = i < job.pieces ? __ldcg(base + i * next + 2 * r) : -INFINITY;
+        top = fmaxf(top, f[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kPromptMostPieces; ++i) {
+        // a NaN stays one; a piece of which the row attends nothing counts for nothing
+        f[i] = f[i] == -INFINITY ? 0.0f : ex2((f[i] - top) * p.scale2);
+        if (f[i] != 0.0f) sum = fmaf(__ldcg(base + i * next + 2 * r + 1), f[i], sum);
+      }
+      const float inv = top == -INFINITY ? 0.0f : 1.0f / sum;
+#pragma unroll 1
+      for (int d = 0; d < HD; d += 32) {
+        float y[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) y[i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kPromptMostPieces; ++k)
+          if (f[k] != 0.0f) {
+            float4 x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              x[i] = __ldcg(reinterpret_cast<const float4*>(base + k * next + 2 * kTile) + (d / 4 + i) * kTile + r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              y[4 * i] = fmaf(x[i].x, f[k], y[4 * i]);
+              y[4 * i + 1] = fmaf(x[i].y, f[k], y[4 * i + 1]);
+              y[4 * i + 2] = fmaf(x[i].z, f[k], y[4 * i + 2]);
+              y[4 * i + 3] = fmaf(x[i].w, f[k], y[4 * i + 3]);
+            }
+          }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) y[i] *= inv;
+        put(d, y);
+      }
+    }
+  }
+  return true;
+}
+
 template <int HD, bool BF16>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     paged_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                        const __grid_constant__ CUtensorMap tmV, const PromptParams p) {
+                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PromptParams p) {
   using Smem = PromptSmem<HD>;
   constexpr int kSlots = Smem::kSlots;
   constexpr uint32_t kIdS = idesc16<BF16>(128, kStep, false), kIdO = idesc16<BF16>(128, HD, true);
-  constexpr int kPartFloats = kTile * (HD + 2);
   extern __shared__ uint8_t smem_raw[];
   // A wait by parity cannot tell a phase from the second one behind it, so every barrier is waited for in
   // each of its phases in turn, or its next phase needs the waiter; what may be two steps behind has two.
   __shared__ uint64_t q_full, q_empty, full[kSlots], empty[kSlots], clean[kSlots];
-  __shared__ uint64_t s_full[2][2], p_full[2][2], o_done[2][2], job_full[2], job_empty[2], part_done[2], part_said[2], fin[2];
+  __shared__ uint64_t s_full[2][2], p_full[2][2], o_done[2][2], job_full[2], job_empty[2], fin[2];
   __shared__ uint32_t tmem_base;
-  __shared__ int abort_flag, last_piece[2];
+  __shared__ int abort_flag;
+  __shared__ Joint joint_mem;
+  Joint* joint = &joint_mem;
   __shared__ Job jobs[2];
   __shared__ int first_block[kPagedMaxLanes + 1];  // of each lane
   uint8_t* qs = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);  // two tiles
@@ -193,8 +359,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         mbar_init(&o_done[t][i], 1);
       }
       mbar_init(&fin[t], 1);
-      mbar_init(&part_done[t], 128);
-      mbar_init(&part_said[t], 1);
+      mbar_init(&joint->done[t], 128);
+      mbar_init(&joint->said[t], 1);
       mbar_init(&job_full[t], 1);
       mbar_init(&job_empty[t], 11);  // warps that read a job
     }
@@ -258,6 +424,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int t = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tbase + lanes + t * 128, to = tbase + lanes + 256 + t * HD;
+    const uint32_t stage = smem_addr(vs + kSlots * Smem::kKv) + warp * 2048;  // 32 rows x 64 bytes
+    const int log_pack = __ffs(p.pack) - 1;
     int c = 0, parts = 0;  // steps of this tile and partial results so far
     bool good = true;
     for (int nj = 0; good; ++nj) {
@@ -265,7 +433,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const Job& job = jobs[nj & 1];
       if (job.lane < 0) break;
       const int first = job.tok0 + t * tq, shift = job.kv - job.n_q;  // shift: position of token 0
-      const int tok = first + r / p.pack, head = job.head0 + r % p.pack;
+      const int tok = first + (r >> log_pack);
       const int lim = min(shift + tok, job.kv - 1);  // last attended position
       const int sure = shift + first;                // attended by every row of the tile
       const int nt = job.n_t[t], pos0 = job.u0 * kStep;
@@ -342,112 +510,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tc_fence_after();
       }
       if (!good) break;
-      const bool attends = nt > 0 && lim >= 0 && m != -INFINITY;
-      const bool store = tok < job.n_q;
-      const int fix0 = max(max(0, shift + job.tok0 + 1), pos0), fix1 = min(lim, pos0 + job.n * kStep - 1);
-      const bool fix = *(volatile const int*)&job.dirty != 0 && store;
-      const int32_t* row = p.table + (size_t)job.seq * s.max_pages;
-      // the values that were taken out of V, for the positions that this row attends
-      auto give_back = [&](int d, float* y) {
-        for (int pos = fix0; pos <= fix1; ++pos) {
-          const uint16_t* src = p.v + ((size_t)row[pos / s.page] * s.kv + job.kvh) * s.block_elems() + (size_t)(pos % s.page) * HD + d;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float v = unpack16<BF16>(src[i]);
-            if (!isfinite(v)) y[i] += v;
-          }
-        }
-      };
-      uint16_t* out = p.out + ((size_t)(job.q0 + tok) * p.n_heads + head) * HD;
-      if (job.pieces == 1) {
-        const float inv = 1.0f / l;
-        if (first < job.n_q) {
-#pragma unroll
-          for (int d = 0; d < HD; d += 16) {
-            uint32_t o[16];
-            if (nt > 0) {  // warp-uniform
-              tmem_ld16(to + d, o);
-              tmem_ld_wait();
-            }
-            float y[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = attends ? __uint_as_float(o[i]) * inv : 0.0f;
-            if (fix) give_back(d, y);
-            if (store) {
-              uint32_t w[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) w[i] = pack16<BF16>(y[2 * i], y[2 * i + 1]);
-              *reinterpret_cast<uint4*>(out + d) = make_uint4(w[0], w[1], w[2], w[3]);
-              *reinterpret_cast<uint4*>(out + d + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-            }
-          }
-        }
-      } else if (first < job.n_q) {
-        // leave the piece's part; the last piece of the tile to come by joins them all in their order
-        float* part = p.part + ((size_t)(job.slot + job.piece) * 2 + t) * kPartFloats;
-        reinterpret_cast<float2*>(part)[r] = make_float2(attends ? m : -INFINITY, l);
-        if (nt > 0) {
-#pragma unroll
-          for (int d = 0; d < HD; d += 16) {
-            uint32_t o[16];
-            tmem_ld16(to + d, o);
-            tmem_ld_wait();
-            float y[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(o[i]);
-            if (fix) give_back(d, y);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) part[2 * kTile + (d + i) * kTile + r] = y[i];
-          }
-        }
-        __threadfence();
-        mbar_arrive(&part_done[t]);
-        if (r == 0 && (good = mbar_wait(&part_done[t], parts & 1, abort_p, kPWait))) {
-          __threadfence();
-          int32_t* count = p.finished + job.slot * 2 + t;
-          const bool last = atomicAdd(count, 1) == job.pieces - 1;
-          if (last) *count = 0;
-          last_piece[t] = last;
-          mbar_arrive(&part_said[t]);
-        }
-        good = __all_sync(0xffffffffu, good && mbar_wait(&part_said[t], parts & 1, abort_p, kPWait));
-        if (!good) break;
-        ++parts;
-        if (*(volatile int*)&last_piece[t]) {
-          __threadfence();
-          const float* base = p.part + ((size_t)job.slot * 2 + t) * kPartFloats;
-          const size_t next = 2 * kPartFloats;  // the following piece's
-          float f[kPromptMostPieces], top = -INFINITY, sum = 0.0f;
-#pragma unroll
-          for (int i = 0; i < kPromptMostPieces; ++i) {
-            f[i] = i < job.pieces ? __ldcg(base + i * next + 2 * r) : -INFINITY;
-            top = fmaxf(top, f[i]);
-          }
-#pragma unroll
-          for (int i = 0; i < kPromptMostPieces; ++i) {
-            // a NaN stays one; a piece of which the row attends nothing counts for nothing
-            f[i] = f[i] == -INFINITY ? 0.0f : ex2((f[i] - top) * p.scale2);
-            if (f[i] != 0.0f) sum = fmaf(__ldcg(base + i * next + 2 * r + 1), f[i], sum);
-          }
-          const float inv = 1.0f / sum;
-          if (store)
-            for (int d = 0; d < HD; d += 8) {
-              float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-              for (int i = 0; i < kPromptMostPieces; ++i)
-                if (f[i] != 0.0f) {
-#pragma unroll
-                  for (int k = 0; k < 8; ++k)
-                    y[k] = fmaf(__ldcg(base + i * next + 2 * kTile + (d + k) * kTile + r), f[i], y[k]);
-                }
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = top == -INFINITY ? 0u : pack16<BF16>(y[2 * k] * inv, y[2 * k + 1] * inv);
-              *reinterpret_cast<uint4*>(out + d) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
-      }
+      if (!(good = finish_rows<HD, BF16>(p, job, t, to, stage, m, l, joint, parts, abort_p))) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&job_empty[nj & 1]);
@@ -550,7 +613,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int items = blocks * subs * p.pieces;
     // Cleans the next V steps of a job that need it, up to step `end`; `first` is the job's first slot.  (This
     // warp waited for the slots to be free, so it knows which phase of their loads it waits for.)
-    constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
+    constexpr uint32_t kExp = BF16 ? 0x7f807f80u : 0x7c007c00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
     int dirty_next = 0;
     auto clean_steps = [&](Job& job, int first, int end) {
       const int every = job.kv - job.n_q + job.tok0;  // the last position that every row attends
@@ -558,26 +621,31 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int i = first + dirty_next + 2, slot = i % kSlots;
         if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], (i / kSlots) & 1, abort_p, kPWait))) return false;
         uint8_t* tile = vs + slot * Smem::kKv;
-        for (int e = lane; e < kStep * HD / 8; e += 32) {
-          const int pos = (job.u0 + dirty_next) * kStep + ((e >> 3) & (kStep - 1));
-          uint4* at = reinterpret_cast<uint4*>(tile + e * 16);  // [half][row][8 chunks]; a row's chunks stay in it
-          if (pos >= job.kv) {
-            *at = make_uint4(0, 0, 0, 0);
-          } else if (pos > every) {
-            uint4 x = *at;
-            uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            bool bad = false;
+        const int pos = (job.u0 + dirty_next) * kStep, end_row = job.kv - pos;  // the first row to zero
+        bool found = false;
+#pragma unroll 4
+        for (int r = max(0, every + 1 - pos) + (lane >> 3); r < kStep; r += 4) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if ((w[k] & kExp) == kExp) bad = true, w[k] &= 0xffff0000u;
-              if (((w[k] >> 16) & kExp) == kExp) bad = true, w[k] &= 0x0000ffffu;
-            }
-            if (bad) {
+          for (int h = 0; h < HD / 64; ++h) {
+            uint4* at = reinterpret_cast<uint4*>(tile + h * (kStep * 128) + r * 128 + (lane & 7) * 16);
+            uint4 x = *at;
+            // a sign bit for every exponent that is all ones
+            const uint32_t bad = (((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) | ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne)) & 0x80008000u;
+            if (r >= end_row) {
+              *at = make_uint4(0, 0, 0, 0);
+            } else if (bad) {
+              uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t b = (w[k] & kExp) + kOne;
+                w[k] &= (b & 0x8000u ? 0u : 0xffffu) | (b & 0x80000000u ? 0u : 0xffff0000u);
+              }
               *at = make_uint4(w[0], w[1], w[2], w[3]);
-              *(volatile int*)&job.dirty = 1;
+              found = true;
             }
           }
         }
+        if (found) *(volatile int*)&job.dirty = 1;
         fence_proxy_async_smem();
         mbar_arrive(&clean[slot]);
       }
