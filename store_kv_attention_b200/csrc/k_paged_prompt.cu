@@ -754,7 +754,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       dirty_next = job.dirty_from;
       const int first = loads;
       good = load_steps(job, &tmK, ks, 0, [&](int w) {
-        if (w == min(kSlots, n + 1)) next = take();  // while the ring is full
+        // while the ring is full, but late: what is taken early is missing where a CTA runs out of work
+        if (w == max(min(kSlots, n + 1), n - kSlots)) next = take();
         return clean_steps(jobs[(nj - 1) & 1], first, w - 5);
       });
     }
