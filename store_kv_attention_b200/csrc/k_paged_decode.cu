@@ -370,14 +370,16 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Deco
   }
 }
 
-// Joins the splits of one (lane, query head): warp w takes splits w, w + 8, ..., a lane four values
-// (HD = 64: half a warp a split).
-constexpr int kJoinWarps = 8;
+// Joins the splits of one (lane, query head): a thread four values of every kAtOnce-th split, eight loads in
+// flight.  (The last CTA of a lane joining its splits inside the kernel above was measured instead: the fence
+// and the counter's round trip stand at the end of every split, 10.1 us a call against 8.9 at one lane of
+// 2049, 193 us against 184 at 32 lanes of 4097.)
+constexpr int kJoinThreads = 256;
 template <int HD, bool BF16>
-__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const DecodeParams p) {
-  constexpr int kLanes = HD / 4, kAtOnce = kJoinWarps * 32 / kLanes;  // splits side by side
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const DecodeParams p) {
+  constexpr int kLanes = HD / 4, kAtOnce = kJoinThreads / kLanes, kWindow = kAtOnce * 8;  // splits a round
   __shared__ float4 part[kAtOnce][kLanes];
-  __shared__ float psum[kAtOnce], pmax[kJoinWarps];
+  __shared__ float weight[kWindow], psum[kJoinThreads / 32], pmax[kJoinThreads / 32];
   ptx::pdl_wait();
   ptx::pdl_trigger();
   const int h = blockIdx.x, b = blockIdx.y, t = threadIdx.x;
@@ -387,42 +389,60 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Decod
   if (n <= 1) return;  // a single split wrote the output itself
   const size_t first = ((size_t)b * p.n_heads + h) * p.s_max;
   const float2* ml = reinterpret_cast<const float2*>(p.ml) + first;
-  float mx = -INFINITY;
-  for (int i = t; i < n; i += 32 * kJoinWarps) mx = fmaxf(mx, ml[i].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if ((t & 31) == 0) pmax[t >> 5] = mx;
-  __syncthreads();
-  mx = pmax[0];
-#pragma unroll
-  for (int w = 1; w < kJoinWarps; ++w) mx = fmaxf(mx, pmax[w]);
   const int d = t % kLanes, g = t / kLanes;
   float4 a = make_float4(0, 0, 0, 0);
-  float sum = 0.0f;
-#pragma unroll 4
-  for (int i = g; i < n; i += kAtOnce) {
-    const float2 s = ml[i];
-    const float4 x = *reinterpret_cast<const float4*>(p.acc + (first + i) * HD + d * 4);
+  float sum = 0.0f, top = -INFINITY;  // of this thread's splits; of all splits so far
+  for (int i0 = 0; i0 < n; i0 += kWindow) {
+    float4 x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = i0 + k * kAtOnce + g;
+      if (i < n) x[k] = *reinterpret_cast<const float4*>(p.acc + (first + i) * HD + d * 4);
+    }
+    const float2 s = t < kWindow && i0 + t < n ? ml[i0 + t] : make_float2(-INFINITY, 0.0f);
+    float mx = s.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if ((t & 31) == 0) pmax[t >> 5] = mx;
+    __syncthreads();
+    mx = top;
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) mx = fmaxf(mx, pmax[w]);
+    const float old = top == -INFINITY ? 0.0f : ex2((top - mx) * p.scale2);
+    top = mx;
     const float f = s.x == -INFINITY ? 0.0f : ex2((s.x - mx) * p.scale2);
-    sum = fmaf(s.y, f, sum);
-    a.x = fmaf(x.x, f, a.x);
-    a.y = fmaf(x.y, f, a.y);
-    a.z = fmaf(x.z, f, a.z);
-    a.w = fmaf(x.w, f, a.w);
+    if (t < kWindow) weight[t] = f;
+    sum = fmaf(sum, old, s.y * f);
+    a = make_float4(a.x * old, a.y * old, a.z * old, a.w * old);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = k * kAtOnce + g;
+      if (i0 + i < n) {
+        a.x = fmaf(x[k].x, weight[i], a.x);
+        a.y = fmaf(x[k].y, weight[i], a.y);
+        a.z = fmaf(x[k].z, weight[i], a.z);
+        a.w = fmaf(x[k].w, weight[i], a.w);
+      }
+    }
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((t & 31) == 0) psum[t >> 5] = sum;
   part[g][d] = a;
-  if (d == 0) psum[g] = sum;
   __syncthreads();
   if (t < kLanes) {
-    sum = psum[0];
+    sum = 0.0f;
 #pragma unroll
-    for (int i = 1; i < kAtOnce; ++i) {
-      const float4 x = part[i][d];
-      sum += psum[i];
-      a.x += x.x;
-      a.y += x.y;
-      a.z += x.z;
-      a.w += x.w;
+    for (int w = 0; w < kJoinThreads / 32; ++w) sum += psum[w];
+    a = make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const float4 y = part[i][d];
+      a.x += y.x;
+      a.y += y.y;
+      a.z += y.z;
+      a.w += y.w;
     }
     const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
     *reinterpret_cast<uint2*>(p.out + ((size_t)b * p.n_heads + h) * HD + d * 4) =
@@ -452,7 +472,7 @@ cudaError_t launch_as(const DecodeParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if (p.s_max > 1) {
     cfg.gridDim = dim3((unsigned)p.n_heads, (unsigned)p.n_lanes);
-    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, paged_join_kernel<HD, BF16>, p);
     count_launch();

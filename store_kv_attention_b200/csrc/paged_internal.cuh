@@ -27,7 +27,7 @@ struct PagedBufs {
 
 // Splits of one lane's `len` positions: target = the splits a lane should have so that the call
 // fills the GPU (0: splits of `fixed` positions).  Otherwise at least ceil(len / kSplitMost)
-// splits, at most one per kSplitLeast positions, of equal length rounded up to 64 positions.
+// splits, at most one per kSplitLeast positions, of equal length rounded up to 16 positions (a warp's unit).
 constexpr int kSplitLeast = 128, kSplitMost = 2048;
 __host__ __device__ inline int paged_split_rows(int len, int target, int fixed) {
   if (target == 0) return fixed;
@@ -36,7 +36,7 @@ __host__ __device__ inline int paged_split_rows(int len, int target, int fixed) 
   n = n > coarse ? n : coarse;
   n = n > 1 ? n : 1;
   const int rows = (len + n - 1) / n;
-  return rows <= 64 ? 64 : (rows + 63) / 64 * 64;
+  return rows <= 16 ? 16 : (rows + 15) / 16 * 16;
 }
 __host__ __device__ inline int paged_splits(int len, int target, int fixed) {
   const int rows = paged_split_rows(len, target, fixed);
