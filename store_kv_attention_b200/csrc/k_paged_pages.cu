@@ -26,32 +26,34 @@ Plan plan_of(const PagedShape& s, uint8_t* ws) {
   return Plan{(uint32_t*)ws, (int32_t*)(ws + w.count_off), (int2*)(ws + w.moves_off), (int32_t*)(ws + w.list_off)};
 }
 
-// Exclusive sum of x over the block's threads in thread order; *total receives the sum.
-__device__ int block_scan(int x, int* total) {
-  __shared__ int part[kPlanThreads / 32];
-  __shared__ int sum;
+// Exclusive sum of x over the block's threads in thread order; *total receives the sum.  (T: int, or long long
+// for several counts side by side.)
+template <typename T>
+__device__ T block_scan(T x, T* total) {
+  __shared__ T part[kPlanThreads / 32];
+  __shared__ T sum;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = x;
+  T incl = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    const T y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
   if (lane == 31) part[warp] = incl;
   __syncthreads();
   if (warp == 0) {
-    const int p = part[lane];
-    int q = p;
+    const T p = part[lane];
+    T q = p;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, q, o);
+      const T y = __shfl_up_sync(0xffffffffu, q, o);
       if (lane >= o) q += y;
     }
     part[lane] = q - p;
     if (lane == 31) sum = q;
   }
   __syncthreads();
-  const int before = part[warp];
+  const T before = part[warp];
   *total = sum;
   __syncthreads();
   return before + incl - x;
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (ok) ok = __ldcg(&plan.list[dst[i]]) == i && __ldcg(&plan.list[src[i]]) == n;
     if (i < n && !ok) atomicOr(plan.status, kStatusRange);
     int total;
-    const int at = made + block_scan(ok, &total);
+    const int at = made + block_scan<int>(ok, &total);
     if (ok) plan.moves[at] = make_int2(src[i], dst[i]);
     made += total;
   }
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(kPlanThreads)
                               const int32_t* n_new, int n) {
   __shared__ int start[kPagedMaxLanes + 1];  // first candidate of each sequence
   __shared__ int first[kPagedMaxLanes];      // its first entry, or -1: refused
-  __shared__ int ids[kPagedMaxLanes];
+  __shared__ __align__(16) int ids[kPagedMaxLanes];
   __shared__ int n_served;                   // sequences that the free pages cover
   ptx::pdl_wait();
   ptx::pdl_trigger();
@@ -246,7 +248,11 @@ __global__ void __launch_bounds__(kPlanThreads)
   int span = 0;
   if (t < n) {
     bool ok = seq >= 0 && seq < s.max_seqs && ctx >= 0 && add >= 0 && (long long)ctx + add <= s.max_len();
-    for (int k = 0; k < t && ok; ++k) ok = ids[k] != seq;
+#pragma unroll 4
+    for (int k = 0; k < t; k += 4) {
+      const int4 x = *reinterpret_cast<const int4*>(ids + k);
+      ok = ok && x.x != seq && (k + 1 >= t || x.y != seq) && (k + 2 >= t || x.z != seq) && (k + 3 >= t || x.w != seq);
+    }
     if (!ok) atomicOr(plan.status, kStatusRange);
     first[t] = ok ? ctx / s.page : 0;
     if (ok && add > 0) span = (ctx + add - 1) / s.page - ctx / s.page + 1;
@@ -283,10 +289,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   for (int base = 0; base < total; base += kPlanThreads) {
     const int i = base + t;
     int was;
-    const bool need = i < total && needs(find(i), i, &was);
-    int sum;
-    block_scan(need, &sum);
-    needed += sum;
+    needed += __syncthreads_count(i < total && needs(find(i), i, &was));
   }
   // the lowest free pages
   const int free_pages =
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       int was, sum;
       const int k = i < total ? find(i) : 0;
       const bool need = i < total && needs(k, i, &was);
-      const int rank = before + block_scan(need, &sum);
+      const int rank = before + block_scan<int>(need, &sum);
       if (need && rank >= free_pages) atomicMin(&n_served, k);
       before += sum;
     }
@@ -318,15 +321,17 @@ __global__ void __launch_bounds__(kPlanThreads)
       k = find(i);
       need = needs(k, i, &was);
     }
-    int sum;
-    const int rank = given + block_scan(need, &sum);
-    given += sum;
     const bool shared = need && was >= 0 && was < s.n_pages;
     const int j = i < end ? first[k] + i - start[k] : 0;
     const bool copy = shared && i == start[k] && (ctx_len[k] % s.page) != 0;  // only its first entry holds rows before ctx_len
+    // needs, copies and drops counted side by side
+    long long sum;
+    const long long at = block_scan<long long>((long long)need | (long long)copy << 20 | (long long)(shared && !copy) << 40, &sum);
+    constexpr int kMask = (1 << 20) - 1;
+    const int rank = given + (int)(at & kMask), mc = (int)(at >> 20 & kMask), md = (int)(at >> 40);
+    const int n_copy = (int)(sum >> 20 & kMask), n_drop = (int)(sum >> 40);
+    given += (int)(sum & kMask);
     const int to = need ? plan.list[rank] : -1;
-    int n_copy, n_drop;
-    const int mc = block_scan(copy, &n_copy), md = block_scan(shared && !copy, &n_drop);
     if (copy) plan.moves[copies + mc] = make_int2(was, to);
     if (shared && !copy) plan.moves[s.n_pages - 1 - (drops + md)] = make_int2(was, to);
     copies += n_copy;
@@ -345,7 +350,9 @@ __global__ void __launch_bounds__(kPlanThreads)
     paged_compact_plan_kernel(PagedShape s, PagedBufs c, Plan plan, int32_t* n_live) {
   ptx::pdl_wait();
   ptx::pdl_trigger();
-  const int live = walk_pages(c.refs, s.n_pages, true, s.n_pages, [](int, int, int) {});
+  int live, mine = 0;
+  for (int p = threadIdx.x; p < s.n_pages; p += kPlanThreads) mine += c.refs[p] > 0;
+  block_scan(mine, &live);
   const int holes = walk_pages(c.refs, live, false, s.n_pages, [&](int p, int, int rank) { plan.moves[rank].y = p; });
   // live pages at or above `live`: as many as there are holes below it
   for (int p = live + threadIdx.x; p < s.n_pages; p += kPlanThreads) plan.list[p] = -1;
