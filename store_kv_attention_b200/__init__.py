@@ -528,6 +528,7 @@ class PagedCache:
         table = torch.full(rows, -1, dtype=torch.int32, device=device) if table is None else table
         refs = torch.zeros(desc.n_pages, dtype=torch.int32, device=device) if refs is None else refs
         self.device, self._index = k.device, k.get_device()
+        self._int32, self._torch_c = torch.int32, torch._C
         for name, t, shape, dt in (("k", k, pool, self.dtype), ("v", v, pool, self.dtype),
                                    ("table", table, rows, torch.int32), ("refs", refs, (desc.n_pages,), torch.int32)):
             _paged_tensor(self, name, t, dt, shape)
@@ -569,36 +570,37 @@ def _paged_rows(cache: PagedCache, name: str, t, n: int, heads: int) -> int:
     return 0
 
 
-def _paged_ints(cache: PagedCache, n: int, **tensors) -> None:
-    import torch
-    for name, t in tensors.items():
-        if t is not None:
-            _paged_tensor(cache, name, t, torch.int32, (n,))
+def _paged_ints(cache: PagedCache, name: str, t, n: int) -> Optional[int]:
+    """The address of t, int32 [n] on the cache's device (None -> NULL)."""
+    if t is None:
+        return None
+    _paged_tensor(cache, name, t, cache._int32, (n,))
+    return t.data_ptr()
 
 
-def _paged_call(cache: PagedCache, name: str, args, stream) -> None:
-    """Calls name(desc, cache, *args, workspace, its size, stream) with the cache's device current; the stream
+def _paged_call(cache: PagedCache, fn: str, args, stream) -> None:
+    """Calls fn(desc, cache, *args, workspace, its size, stream) with the cache's device current; the stream
     None is that device's current one."""
-    import torch
-    if torch.cuda.current_device() != cache._index:
+    c = cache._torch_c
+    if c._cuda_getDevice() != cache._index:
+        import torch
         with torch.cuda.device(cache._index):
-            return _paged_call(cache, name, args, stream)
-    raw = torch._C._cuda_getCurrentRawStream(cache._index) if stream is None else _stream(stream)
-    st = getattr(_lib_handle or _load(), name)(*cache._head, *args, *cache._tail, raw)
+            return _paged_call(cache, fn, args, stream)
+    raw = c._cuda_getCurrentRawStream(cache._index) if stream is None else _stream(stream)
+    st = getattr(_lib_handle, fn)(*cache._head, *args, *cache._tail, raw)
     if st != TL_OK:
-        _check(st, name)
+        _check(st, fn)
 
 
 def paged_append(cache: PagedCache, layer: int, k_rows, v_rows, start_pos, cu_rows=None, seqs=None, stream=None) -> None:
     """tl_paged_append: k_rows, v_rows [n, n_kv_heads, head_dim] in the cache's type (rows may be strided);
     start_pos / seqs int32 [n_lanes], cu_rows int32 [n_lanes + 1] (None: one row per lane)."""
-    rows, n = k_rows.shape[0], start_pos.numel()
+    rows, n = k_rows.shape[0], start_pos.shape[0]
     ks = _paged_rows(cache, "k_rows", k_rows, rows, cache.desc.n_kv_heads)
     vs = _paged_rows(cache, "v_rows", v_rows, rows, cache.desc.n_kv_heads)
-    _paged_ints(cache, n, start_pos=start_pos, seqs=seqs)
-    _paged_ints(cache, n + 1, cu_rows=cu_rows)
-    _paged_call(cache, "tl_paged_append", (layer, _ptr(k_rows), ks, _ptr(v_rows), vs, rows, _ptr(cu_rows),
-                                           _ptr(start_pos), _ptr(seqs), n), stream)
+    _paged_call(cache, "tl_paged_append",
+                (layer, k_rows.data_ptr(), ks, v_rows.data_ptr(), vs, rows, _paged_ints(cache, "cu_rows", cu_rows, n + 1),
+                 _paged_ints(cache, "start_pos", start_pos, n), _paged_ints(cache, "seqs", seqs, n), n), stream)
 
 
 def paged_attn_decode(cache: PagedCache, layer: int, q, kv_len, out, seqs=None, scale: float = 0.0, stream=None) -> None:
@@ -607,53 +609,50 @@ def paged_attn_decode(cache: PagedCache, layer: int, q, kv_len, out, seqs=None, 
     n, heads = q.shape[0], q.shape[1]
     qs = _paged_rows(cache, "q", q, n, heads)
     _paged_tensor(cache, "out", out, cache.dtype, (n, heads, cache.desc.head_dim))
-    _paged_ints(cache, n, kv_len=kv_len, seqs=seqs)
-    _paged_call(cache, "tl_paged_attn_decode", (layer, heads, _ptr(q), qs, _ptr(kv_len), _ptr(seqs), float(scale),
-                                                cache.split_rows, _ptr(out), n), stream)
+    _paged_call(cache, "tl_paged_attn_decode",
+                (layer, heads, q.data_ptr(), qs, _paged_ints(cache, "kv_len", kv_len, n), _paged_ints(cache, "seqs", seqs, n),
+                 scale, cache.split_rows, out.data_ptr(), n), stream)
 
 
 def paged_prompt_attn(cache: PagedCache, layer: int, q, cu_q, kv_len, out, seqs=None, scale: float = 0.0,
                       stream=None) -> None:
     """tl_paged_prompt_attn: packed queries q [n, n_heads, head_dim] (rows may be strided), cu_q int32
     [n_lanes + 1], kv_len / seqs int32 [n_lanes], out [n, n_heads, head_dim]."""
-    n, heads, lanes = q.shape[0], q.shape[1], kv_len.numel()
+    n, heads, lanes = q.shape[0], q.shape[1], kv_len.shape[0]
     qs = _paged_rows(cache, "q", q, n, heads)
     _paged_tensor(cache, "out", out, cache.dtype, (n, heads, cache.desc.head_dim))
-    _paged_ints(cache, lanes, kv_len=kv_len, seqs=seqs)
-    _paged_ints(cache, lanes + 1, cu_q=cu_q)
-    _paged_call(cache, "tl_paged_prompt_attn", (layer, heads, _ptr(q), qs, n, _ptr(cu_q), _ptr(kv_len), _ptr(seqs),
-                                                float(scale), _ptr(out), lanes), stream)
+    _paged_call(cache, "tl_paged_prompt_attn",
+                (layer, heads, q.data_ptr(), qs, n, _paged_ints(cache, "cu_q", cu_q, lanes + 1),
+                 _paged_ints(cache, "kv_len", kv_len, lanes), _paged_ints(cache, "seqs", seqs, lanes), scale, out.data_ptr(),
+                 lanes), stream)
 
 
 def paged_copy(cache: PagedCache, src, dst, stream=None) -> None:
     """tl_paged_copy: page src[i] to page dst[i] (int32 [n], device), every layer's K and V."""
-    n = src.numel()
-    _paged_ints(cache, n, src=src, dst=dst)
-    _paged_call(cache, "tl_paged_copy", (_ptr(src), _ptr(dst), n), stream)
+    n = src.shape[0]
+    _paged_call(cache, "tl_paged_copy", (_paged_ints(cache, "src", src, n), _paged_ints(cache, "dst", dst, n), n), stream)
 
 
 def paged_fork(cache: PagedCache, src, dst, n_tokens, stream=None) -> None:
     """tl_paged_fork: sequence dst[i] shares the first n_tokens[i] positions of src[i] (int32 [n], device)."""
-    n = src.numel()
-    _paged_ints(cache, n, src=src, dst=dst, n_tokens=n_tokens)
-    _paged_call(cache, "tl_paged_fork", (_ptr(src), _ptr(dst), _ptr(n_tokens), n), stream)
+    n = src.shape[0]
+    _paged_call(cache, "tl_paged_fork", (_paged_ints(cache, "src", src, n), _paged_ints(cache, "dst", dst, n),
+                                         _paged_ints(cache, "n_tokens", n_tokens, n), n), stream)
 
 
 def paged_reserve(cache: PagedCache, seqs, ctx_len, n_new, stream=None) -> None:
     """tl_paged_reserve: pages of its own for positions ctx_len[i] .. + n_new[i] - 1 of sequence seqs[i]."""
-    n = seqs.numel()
-    _paged_ints(cache, n, seqs=seqs, ctx_len=ctx_len, n_new=n_new)
-    _paged_call(cache, "tl_paged_reserve", (_ptr(seqs), _ptr(ctx_len), _ptr(n_new), n), stream)
+    n = seqs.shape[0]
+    _paged_call(cache, "tl_paged_reserve", (_paged_ints(cache, "seqs", seqs, n), _paged_ints(cache, "ctx_len", ctx_len, n),
+                                            _paged_ints(cache, "n_new", n_new, n), n), stream)
 
 
 def paged_free(cache: PagedCache, seqs, keep=None, stream=None) -> None:
     """tl_paged_free: the pages behind the first keep[i] positions (None: all) of sequence seqs[i]."""
-    n = seqs.numel()
-    _paged_ints(cache, n, seqs=seqs, keep=keep)
-    _paged_call(cache, "tl_paged_free", (_ptr(seqs), _ptr(keep), n), stream)
+    n = seqs.shape[0]
+    _paged_call(cache, "tl_paged_free", (_paged_ints(cache, "seqs", seqs, n), _paged_ints(cache, "keep", keep, n), n), stream)
 
 
 def paged_compact(cache: PagedCache, n_live=None, stream=None) -> None:
     """tl_paged_compact: the pages in use become pages 0 .. n - 1; n_live (int32 [1]) receives n."""
-    _paged_ints(cache, 1, n_live=n_live)
-    _paged_call(cache, "tl_paged_compact", (_ptr(n_live),), stream)
+    _paged_call(cache, "tl_paged_compact", (_paged_ints(cache, "n_live", n_live, 1),), stream)

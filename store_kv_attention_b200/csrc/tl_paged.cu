@@ -153,19 +153,19 @@ tl_status tl_paged_append(const tl_paged_desc* desc, tl_paged_cache cache, int32
   tl_status st = check_desc(desc, &s);
   if (st != TL_OK) return st;
   if ((st = check_cache(cache, false)) != TL_OK) return st;
+  if (n_rows < 0) return set_error(TL_ERR_INVALID_ARG, "n_rows %d < 0", n_rows);
+  if (n_rows == 0) return check_layer(s, layer);  // nothing to write (an empty array may have no address)
   if (!k_rows || !v_rows || !start_pos) return set_error(TL_ERR_INVALID_ARG, "k_rows / v_rows / start_pos is NULL");
   if (!aligned(k_rows, 16) || !aligned(v_rows, 16))
     return set_error(TL_ERR_INVALID_ARG, "k_rows and v_rows must be 16-byte aligned");
   if ((st = check_layer(s, layer)) != TL_OK) return st;
   if ((st = check_lanes(s, n_lanes, seqs)) != TL_OK) return st;
-  if (n_rows < 0) return set_error(TL_ERR_INVALID_ARG, "n_rows %d < 0", n_rows);
   if (!cu_rows && n_rows != n_lanes)
     return set_error(TL_ERR_INVALID_ARG, "n_rows %d != n_lanes %d without cu_rows", n_rows, n_lanes);
   const int64_t dense = (int64_t)s.kv * s.hd;
   if ((st = check_stride(&k_stride, dense, "k_stride")) != TL_OK) return st;
   if ((st = check_stride(&v_stride, dense, "v_stride")) != TL_OK) return st;
   if ((st = check_workspace(workspace, workspace_bytes, 256)) != TL_OK) return st;
-  if (n_rows == 0) return TL_OK;
   cudaError_t e = tl::launch_paged_append(s, bufs(cache), layer, k_rows, k_stride, v_rows, v_stride, n_rows, cu_rows,
                                           start_pos, seqs, n_lanes, (uint32_t*)workspace, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_error(e, "tl_paged_append launch");
@@ -207,12 +207,13 @@ tl_status tl_paged_prompt_attn(const tl_paged_desc* desc, tl_paged_cache cache, 
   tl_status st = check_desc(desc, &s);
   if (st != TL_OK) return st;
   if ((st = check_cache(cache, false)) != TL_OK) return st;
+  if (n_rows < 0) return set_error(TL_ERR_INVALID_ARG, "n_rows %d < 0", n_rows);
+  if (n_rows == 0) return check_layer(s, layer);  // no queries
   if (!q || !cu_q || !kv_len || !out) return set_error(TL_ERR_INVALID_ARG, "q / cu_q / kv_len / out is NULL");
   if (!aligned(q, 16) || !aligned(out, 16)) return set_error(TL_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
   if ((st = check_layer(s, layer)) != TL_OK) return st;
   if ((st = check_heads(s, n_heads)) != TL_OK) return st;
   if ((st = check_lanes(s, n_lanes, seqs)) != TL_OK) return st;
-  if (n_rows < 0) return set_error(TL_ERR_INVALID_ARG, "n_rows %d < 0", n_rows);
   if (n_rows > (1 << 24)) return set_error(TL_ERR_UNSUPPORTED, "n_rows %d > 2^24", n_rows);
   if ((st = check_stride(&q_stride, (int64_t)n_heads * s.hd, "q_stride")) != TL_OK) return st;
   if ((st = check_scale(&scale, s.hd)) != TL_OK) return st;
@@ -220,7 +221,6 @@ tl_status tl_paged_prompt_attn(const tl_paged_desc* desc, tl_paged_cache cache, 
   if ((st = check_workspace(workspace, workspace_bytes, plan.total)) != TL_OK) return st;
   if (plan.blocks > INT32_MAX / 4)
     return set_error(TL_ERR_UNSUPPORTED, "%d rows of %d heads in one call", n_rows, n_heads);
-  if (n_rows == 0) return TL_OK;
   const tl::PagedPromptArgs a{s, bufs(cache), layer, n_heads, n_lanes, n_rows, q, q_stride, cu_q,
                               kv_len, seqs, scale, out, (uint8_t*)workspace, plan};
   cudaError_t e = tl::launch_paged_prompt(a, (cudaStream_t)stream);
@@ -233,8 +233,8 @@ tl_status tl_paged_copy(const tl_paged_desc* desc, tl_paged_cache cache, const i
   PagedShape s{};
   tl_status st = check_op(desc, cache, n, desc ? desc->n_pages : 0, workspace, workspace_bytes, &s);
   if (st != TL_OK) return st;
-  if (!src || !dst) return set_error(TL_ERR_INVALID_ARG, "src / dst is NULL");
   if (n == 0) return TL_OK;
+  if (!src || !dst) return set_error(TL_ERR_INVALID_ARG, "src / dst is NULL");
   cudaError_t e = tl::launch_paged_copy(s, bufs(cache), src, dst, n, (uint8_t*)workspace, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_error(e, "tl_paged_copy launch");
   return TL_OK;
@@ -246,8 +246,8 @@ tl_status tl_paged_fork(const tl_paged_desc* desc, tl_paged_cache cache, const i
   PagedShape s{};
   tl_status st = check_op(desc, cache, n, tl::kPagedMaxLanes, workspace, workspace_bytes, &s);
   if (st != TL_OK) return st;
-  if (!src || !dst || !n_tokens) return set_error(TL_ERR_INVALID_ARG, "src / dst / n_tokens is NULL");
   if (n == 0) return TL_OK;
+  if (!src || !dst || !n_tokens) return set_error(TL_ERR_INVALID_ARG, "src / dst / n_tokens is NULL");
   cudaError_t e = tl::launch_paged_fork(s, bufs(cache), src, dst, n_tokens, n, (uint8_t*)workspace, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_error(e, "tl_paged_fork launch");
   return TL_OK;
@@ -259,8 +259,8 @@ tl_status tl_paged_reserve(const tl_paged_desc* desc, tl_paged_cache cache, cons
   PagedShape s{};
   tl_status st = check_op(desc, cache, n, tl::kPagedMaxLanes, workspace, workspace_bytes, &s);
   if (st != TL_OK) return st;
-  if (!seqs || !ctx_len || !n_new) return set_error(TL_ERR_INVALID_ARG, "seqs / ctx_len / n_new is NULL");
   if (n == 0) return TL_OK;
+  if (!seqs || !ctx_len || !n_new) return set_error(TL_ERR_INVALID_ARG, "seqs / ctx_len / n_new is NULL");
   cudaError_t e = tl::launch_paged_reserve(s, bufs(cache), seqs, ctx_len, n_new, n, (uint8_t*)workspace, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_error(e, "tl_paged_reserve launch");
   return TL_OK;
@@ -271,8 +271,8 @@ tl_status tl_paged_free(const tl_paged_desc* desc, tl_paged_cache cache, const i
   PagedShape s{};
   tl_status st = check_op(desc, cache, n, tl::kPagedMaxLanes, workspace, workspace_bytes, &s);
   if (st != TL_OK) return st;
-  if (!seqs) return set_error(TL_ERR_INVALID_ARG, "seqs is NULL");
   if (n == 0) return TL_OK;
+  if (!seqs) return set_error(TL_ERR_INVALID_ARG, "seqs is NULL");
   cudaError_t e = tl::launch_paged_free(s, bufs(cache), seqs, keep, n, (uint8_t*)workspace, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_error(e, "tl_paged_free launch");
   return TL_OK;

@@ -79,7 +79,8 @@ def test_calls_rejected_before_launch(tl):
     assert append(n=9, rows=9) == tl.TL_ERR_CAPACITY            # more lanes than sequences
     assert append(n=1025, rows=1025, seqs=fake) == tl.TL_ERR_UNSUPPORTED
     assert append(w=None) == tl.TL_ERR_INVALID_ARG and append(wb=128) == tl.TL_ERR_CAPACITY
-    assert append(rows=0, cu=fake) == tl.TL_OK
+    assert append(rows=0, cu=fake) == tl.TL_OK and append(rows=0, k=None, start=None) == tl.TL_OK
+    assert append(rows=0, layer=3) == tl.TL_ERR_CAPACITY
 
     def decode(layer=0, heads=8, q=fake, qs=0, lens=fake, scale=0.0, split=0, out=fake, n=4, w=fake, wb=ws):
         return L.tl_paged_attn_decode(dc, c, layer, heads, q, qs, lens, None, scale, split, out, n, w, wb, None)
@@ -111,6 +112,7 @@ def test_calls_rejected_before_launch(tl):
         assert f(dc, c, *args, 1, fake, 256, None) == tl.TL_ERR_CAPACITY
         assert f(dc, c, None, *args[1:], 1, fake, ws, None) == tl.TL_ERR_INVALID_ARG
         assert f(dc, c, *args, 0, fake, ws, None) == tl.TL_OK
+        assert f(dc, c, *[None] * len(args), 0, fake, ws, None) == tl.TL_OK   # an empty list has no address
     assert L.tl_paged_compact(dc, no_refs, None, fake, ws, None) == tl.TL_ERR_INVALID_ARG
     assert L.tl_paged_compact(dc, c, None, fake, 256, None) == tl.TL_ERR_CAPACITY
 
