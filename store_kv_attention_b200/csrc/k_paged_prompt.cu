@@ -75,7 +75,7 @@ struct PromptSmem {
   static constexpr int kQ = kTile * HD * 2;     // one tile of queries
   static constexpr int kKv = kStep * HD * 2;    // one step of K or of V
   static constexpr int kSlots = 4;              // of each ring
-  static constexpr int kStage = 8 * 32 * 64;    // of the outputs, a softmax warp's rows x 32 values
+  static constexpr int kStage = 8 * 2 * 32 * 64;  // of the outputs, a softmax warp's rows x 32 values, twice
   static constexpr int kBytes = 1024 + 2 * kQ + 2 * kSlots * kKv + kStage;
 };
 
@@ -165,11 +165,12 @@ struct Joint {
 // workspace and, by the last piece, the parts joined.  (A function of its own, so that its registers are not
 // the softmax loop's.)  False: a wait gave up.
 template <int HD, bool BF16>
-__device__ __noinline__ bool finish_rows(const PromptParams& p, const Job& job, int t, uint32_t to, uint32_t stage,
-                                         float m, float l, Joint* joint, int& parts, volatile int* abort) {
+__device__ __noinline__ bool finish_rows(const PromptParams& p, const CUtensorMap* tmO, const Job& job, int t,
+                                         int log_pack, uint32_t to, uint32_t stage, float m, float l, Joint* joint,
+                                         int& parts, volatile int* abort) {
   constexpr int kPartFloats = kTile * (HD + 2);
   const PagedShape& s = p.s;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x & 127, log_pack = __ffs(p.pack) - 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x & 127;
   const int tq = kTile >> log_pack, first = job.tok0 + t * tq, shift = job.kv - job.n_q;
   const int tok = first + (r >> log_pack), lim = min(shift + tok, job.kv - 1);
   const int nt = job.n_t[t], pos0 = job.u0 * kStep;
@@ -190,33 +191,46 @@ __device__ __noinline__ bool finish_rows(const PromptParams& p, const Job& job, 
       }
     }
   };
-  // 32 values of every row of the warp through shared memory, so that four lanes write 64 bytes of a row:
-  // this lane 16 bytes of rows lane / 4 + 0, 8, 16 and 24
-  uint16_t* dst[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = (warp & 3) * 32 + i * 8 + (lane >> 2), to_tok = first + (row >> log_pack);
-    dst[i] = to_tok < job.n_q ? p.out + ((size_t)(job.q0 + to_tok) * p.n_heads + job.head0 + (row & (p.pack - 1))) * HD + (lane & 3) * 8 : nullptr;
-  }
-  const uint32_t put_at = stage + lane * 64, get_at = stage + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+  // 32 values of every row of the warp through shared memory (64-byte rows, 64-byte swizzle), in two buffers by
+  // turns: one TMA store where all rows are the lane's, else four lanes write 64 bytes of a row
+  const int row0 = (warp & 3) * 32;
+  const bool all = first + ((row0 + 31) >> log_pack) < job.n_q;
+  const int to_head = job.head0 + (row0 & ((1 << log_pack) - 1)), to_row = job.q0 + first + (row0 >> log_pack);
   auto put = [&](int d, const float* y) {
+    const uint32_t buf = stage + (d / 32 & 1) * 2048;
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the store before the last has read this buffer
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(put_at + ((i ^ ((lane >> 1) & 3)) << 4)),
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)),
                    "r"(pack16<BF16>(y[8 * i], y[8 * i + 1])), "r"(pack16<BF16>(y[8 * i + 2], y[8 * i + 3])),
                    "r"(pack16<BF16>(y[8 * i + 4], y[8 * i + 5])), "r"(pack16<BF16>(y[8 * i + 6], y[8 * i + 7]))
                    : "memory");
+    if (all) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                         reinterpret_cast<uint64_t>(tmO)),
+                     "r"(d), "r"(to_head), "r"(to_row), "r"(buf)
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+      return;
+    }
     __syncwarp();
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < 4; ++i) {
+      const int wr = i * 8 + (lane >> 2), row = row0 + wr, to_tok = first + (row >> log_pack);
       uint4 v;
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                   : "r"(get_at + i * 512)
+                   : "r"(buf + wr * 64 + (((lane & 3) ^ ((wr >> 1) & 3)) << 4))
                    : "memory");
-      if (dst[i]) *reinterpret_cast<uint4*>(dst[i] + d) = v;
+      if (to_tok < job.n_q)
+        *reinterpret_cast<uint4*>(p.out + ((size_t)(job.q0 + to_tok) * p.n_heads + job.head0 + (row & ((1 << log_pack) - 1))) * HD + d +
+                                  (lane & 3) * 8) = v;
     }
-    __syncwarp();
   };
   if (first >= job.n_q) {
     // a tile without tokens
@@ -322,7 +336,8 @@ __device__ __noinline__ bool finish_rows(const PromptParams& p, const Job& job, 
 template <int HD, bool BF16>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     paged_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PromptParams p) {
+                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                        const __grid_constant__ PromptParams p) {
   using Smem = PromptSmem<HD>;
   constexpr int kSlots = Smem::kSlots;
   constexpr uint32_t kIdS = idesc16<BF16>(128, kStep, false), kIdO = idesc16<BF16>(128, HD, true);
@@ -336,7 +351,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   __shared__ Joint joint_mem;
   Joint* joint = &joint_mem;
   __shared__ Job jobs[2];
-  __shared__ int first_block[kPagedMaxLanes + 1];  // of each lane
   uint8_t* qs = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);  // two tiles
   uint8_t* ks = qs + 2 * Smem::kQ;
   uint8_t* vs = ks + kSlots * Smem::kKv;
@@ -424,7 +438,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int t = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tbase + lanes + t * 128, to = tbase + lanes + 256 + t * HD;
-    const uint32_t stage = smem_addr(vs + kSlots * Smem::kKv) + warp * 2048;  // 32 rows x 64 bytes
+    const uint32_t stage = smem_addr(vs + kSlots * Smem::kKv) + warp * 4096;  // twice 32 rows x 64 bytes
     const int log_pack = __ffs(p.pack) - 1;
     int c = 0, parts = 0;  // steps of this tile and partial results so far
     bool good = true;
@@ -510,11 +524,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tc_fence_after();
       }
       if (!good) break;
-      if (!(good = finish_rows<HD, BF16>(p, job, t, to, stage, m, l, joint, parts, abort_p))) break;
+      if (!(good = finish_rows<HD, BF16>(p, &tmO, job, t, log_pack, to, stage, m, l, joint, parts, abort_p))) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&job_empty[nj & 1]);
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the outputs are written
   } else if (warp == 8 || warp == 11) {
     // ------------------------------------------------------------ products of tile t
     const int t = warp == 11;
@@ -586,30 +601,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ work and loads
-    // the lanes' blocks of 2 x tq tokens
+    // the blocks of 2 x tq tokens of 32 lanes at a time; a lane whose rows are out of range has none
+    auto blocks_of = [&](int b, bool note) {
+      if (b >= p.n_lanes) return 0;
+      const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
+      if (q0 >= 0 && q1 <= p.n_rows && q1 >= q0) return (q1 - q0 + 2 * tq - 1) / (2 * tq);
+      if (note) atomicOr(p.status, kStatusRange);
+      return 0;
+    };
     int blocks = 0;
-    for (int base = 0; base < p.n_lanes; base += 32) {
-      const int b = base + lane;
-      int n = 0;
-      if (b < p.n_lanes) {
-        const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
-        if (q0 < 0 || q1 > p.n_rows || q1 < q0) {
-          if (blockIdx.x == 0) atomicOr(p.status, kStatusRange);
-        } else {
-          n = (q1 - q0 + 2 * tq - 1) / (2 * tq);
-        }
-      }
-      int incl = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      if (b < p.n_lanes) first_block[b] = blocks + incl - n;
-      blocks += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (lane == 0) first_block[p.n_lanes] = blocks;
-    __syncwarp();
+    for (int base = 0; base < p.n_lanes; base += 32) blocks += __reduce_add_sync(0xffffffffu, blocks_of(base + lane, blockIdx.x == 0));
+    int scan_base = 0, scan_done = 0;  // items only grow: the scan for a lane goes on where the last one stopped
     const int items = blocks * subs * p.pieces;
     // Cleans the next V steps of a job that need it, up to step `end`; `first` is the job's first slot.  (This
     // warp waited for the slots to be free, so it knows which phase of their loads it waits for.)
@@ -660,13 +662,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         int more = 0;
         if (lane == 0) more = gridDim.x + atomicAdd(p.queue, 1);
         item = __shfl_sync(0xffffffffu, more, 0);
-        int b = 0, hi = p.n_lanes;
-        while (hi - b > 1) {
-          const int mid = (b + hi) >> 1;
-          if (first_block[mid] <= blk)
-            b = mid;
-          else
-            hi = mid;
+        int b, after;  // the block's lane, the blocks up to its last
+        for (;; scan_base += 32) {
+          int incl = blocks_of(scan_base + lane, false);
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+          }
+          const unsigned has = __ballot_sync(0xffffffffu, blk < scan_done + incl);
+          if (has) {
+            b = scan_base + __ffs(has) - 1;
+            after = scan_done + __shfl_sync(0xffffffffu, incl, __ffs(has) - 1);
+            break;
+          }
+          scan_done += __shfl_sync(0xffffffffu, incl, 31);
         }
         job.q0 = p.cu_q[b];
         job.n_q = p.cu_q[b + 1] - job.q0;
@@ -687,7 +697,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (lane == 0) atomicOr(p.status, kStatusRange);
           continue;
         }
-        job.tok0 = (first_block[b + 1] - 1 - blk) * 2 * tq;  // a lane's last block first
+        job.tok0 = (after - 1 - blk) * 2 * tq;  // a lane's last block first
         job.head0 = sub * p.pack;
         job.kvh = job.head0 / p.group;
         const int shift = job.kv - job.n_q;
@@ -819,20 +829,22 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// 16-bit tensor map [z][y][x], row pitches in bytes, box [box_z][box_y][64], 128-byte swizzle.
+// 16-bit tensor map [z][y][x], row pitches in bytes, box [box_z][box_y][box_x], swizzled by the box's rows (64
+// values: 128 bytes, 32: 64).
 bool make_tmap3(CUtensorMap* tm, const void* base, bool bf16, uint64_t x, uint64_t y, uint64_t z, uint64_t pitch_y,
-                uint64_t pitch_z, uint32_t box_y, uint32_t box_z) {
+                uint64_t pitch_z, uint32_t box_y, uint32_t box_z, uint32_t box_x = 64) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[3] = {x, y, z}, strides[2] = {pitch_y, pitch_z};
-  const cuuint32_t box[3] = {64, box_y, box_z}, estr[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {box_x, box_y, box_z}, estr[3] = {1, 1, 1};
   return enc(tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base),
-             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             box_x == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int HD, bool BF16>
-cudaError_t launch_as(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, const PromptParams& p,
+cudaError_t launch_as(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, const CUtensorMap& tmO,
+                      const PromptParams& p,
                       long long blocks, cudaStream_t st) {
   int limit = 0;
   cudaError_t e = dyn_smem_limit((const void*)paged_prompt_kernel<HD, BF16>, &limit);
@@ -847,7 +859,7 @@ cudaError_t launch_as(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUte
   cfg.blockDim = dim3(kPromptThreads);
   cfg.dynamicSmemBytes = PromptSmem<HD>::kBytes;
   profile_stream_begin(st);
-  e = cudaLaunchKernelEx(&cfg, paged_prompt_kernel<HD, BF16>, tmQ, tmK, tmV, p);
+  e = cudaLaunchKernelEx(&cfg, paged_prompt_kernel<HD, BF16>, tmQ, tmK, tmV, tmO, p);
   profile_stream_end(st);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -861,12 +873,14 @@ cudaError_t launch_paged_prompt(const PagedPromptArgs& a, cudaStream_t st) {
   const int group = a.n_heads / s.kv;
   const int pack = prompt_pack(s, a.n_heads);
   const bool bf16 = s.dtype == TL_KV_BF16;
-  alignas(64) CUtensorMap tmQ, tmK, tmV;
+  alignas(64) CUtensorMap tmQ, tmK, tmV, tmO;
   const uint64_t rows = (uint64_t)s.n_pages * s.kv;
   const uint32_t box = s.page < kStep ? s.page : kStep;
   if (!make_tmap3(&tmQ, a.q, bf16, s.hd, a.n_heads, a.n_rows, s.hd * 2, (uint64_t)a.q_stride * 2, pack, kTile / pack) ||
       !make_tmap3(&tmK, a.c.k + off, bf16, s.hd, s.page, rows, s.hd * 2, s.block_elems() * 2, box, 1) ||
-      !make_tmap3(&tmV, a.c.v + off, bf16, s.hd, s.page, rows, s.hd * 2, s.block_elems() * 2, box, 1))
+      !make_tmap3(&tmV, a.c.v + off, bf16, s.hd, s.page, rows, s.hd * 2, s.block_elems() * 2, box, 1) ||
+      !make_tmap3(&tmO, a.out, bf16, s.hd, a.n_heads, a.n_rows, s.hd * 2, (uint64_t)a.n_heads * s.hd * 2,
+                  pack < 32 ? pack : 32, pack < 32 ? 32 / pack : 1, 32))
     return cudaErrorInvalidValue;
   const PromptParams p{s,
                        a.c.v + off,
@@ -887,8 +901,8 @@ cudaError_t launch_paged_prompt(const PagedPromptArgs& a, cudaStream_t st) {
                        a.n_lanes,
                        a.plan.pieces};
   if (s.hd == 64)
-    return bf16 ? launch_as<64, true>(tmQ, tmK, tmV, p, a.plan.blocks, st) : launch_as<64, false>(tmQ, tmK, tmV, p, a.plan.blocks, st);
-  return bf16 ? launch_as<128, true>(tmQ, tmK, tmV, p, a.plan.blocks, st) : launch_as<128, false>(tmQ, tmK, tmV, p, a.plan.blocks, st);
+    return bf16 ? launch_as<64, true>(tmQ, tmK, tmV, tmO, p, a.plan.blocks, st) : launch_as<64, false>(tmQ, tmK, tmV, tmO, p, a.plan.blocks, st);
+  return bf16 ? launch_as<128, true>(tmQ, tmK, tmV, tmO, p, a.plan.blocks, st) : launch_as<128, false>(tmQ, tmK, tmV, tmO, p, a.plan.blocks, st);
 }
 
 }  // namespace tl
