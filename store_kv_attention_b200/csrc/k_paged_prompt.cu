@@ -609,10 +609,28 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (note) atomicOr(p.status, kStatusRange);
       return 0;
     };
-    int blocks = 0;
-    for (int base = 0; base < p.n_lanes; base += 32) blocks += __reduce_add_sync(0xffffffffu, blocks_of(base + lane, blockIdx.x == 0));
+    int blocks = 0, longest = 0;
+    for (int base = 0; base < p.n_lanes; base += 32) {
+      blocks += __reduce_add_sync(0xffffffffu, blocks_of(base + lane, blockIdx.x == 0));
+      if (base + lane < p.n_lanes) longest = max(longest, p.kv_len[base + lane]);
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
     int scan_base = 0, scan_done = 0;  // items only grow: the scan for a lane goes on where the last one stopped
-    const int items = blocks * subs * p.pieces;
+    // Blocks beyond the last full round over the CTAs are cut into `cut` pieces (a short one into fewer), so that
+    // they take less than a round of their own: the least of rounds x (piece + what a piece costs besides).  Not
+    // where most blocks are too short for it: every piece that there is not is work taken in vain.
+    const int sms = gridDim.x, whole = blocks * subs / sms * sms, rest = blocks * subs - whole;
+    int cut = 1;
+    float best = 1.0f;
+    for (int r = 1; r < 4 && rest > 0; ++r) {
+      const int c = min(min(p.pieces, longest / (2 * kPieceSteps * kStep)), min(r * sms, kPromptPieces) / rest);
+      const float cost = (float)((rest * c + sms - 1) / sms) * (1.0f / (float)c + 0.05f);
+      if (c > 1 && cost < best) {
+        cut = c;
+        best = cost;
+      }
+    }
+    const int items = whole + rest * cut;
     // Cleans the next V steps of a job that need it, up to step `end`; `first` is the job's first slot.  (This
     // warp waited for the slots to be free, so it knows which phase of their loads it waits for.)
     constexpr uint32_t kExp = BF16 ? 0x7f807f80u : 0x7c007c00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
@@ -658,7 +676,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       Job job = {};
       job.lane = -1;
       while (item < items) {
-        const int piece = item % p.pieces, bs = item / p.pieces, sub = bs % subs, blk = bs / subs;
+        const int over = max(0, item - whole), piece = over % cut, bs = min(item, whole) + over / cut;
+        const int most = item < whole ? 1 : cut, sub = bs % subs, blk = bs / subs;
         int more = 0;
         if (lane == 0) more = gridDim.x + atomicAdd(p.queue, 1);
         item = __shfl_sync(0xffffffffu, more, 0);
@@ -709,11 +728,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           n_t[t] = first < job.n_q && last >= 0 ? last / kStep + 1 : 0;
         }
         const int all = max(n_t[0], n_t[1]);
-        job.pieces = max(1, min(p.pieces, all / kPieceSteps));
+        job.pieces = max(1, min(most, all / kPieceSteps));
         if (piece >= job.pieces) continue;
         const int each = (all + job.pieces - 1) / job.pieces;
         job.piece = piece;
-        job.slot = bs * p.pieces;
+        job.slot = (bs - whole) * cut;
         job.u0 = piece * each;
         job.n = max(0, min(each, all - job.u0));
         for (int t = 0; t < 2; ++t) job.n_t[t] = max(0, min(job.n, n_t[t] - job.u0));

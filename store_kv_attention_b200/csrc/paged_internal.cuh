@@ -81,9 +81,9 @@ inline size_t paged_workspace_upto(const PagedShape& s, int n_heads, int n_lanes
   return align256(align256(kPagedHead + parts * 8) + parts * s.hd * 4);
 }
 // Prompt attention: heads packed into a tile's rows (the largest power of two up to 128 that divides the
-// group), blocks of two tiles there can be, and the pieces that a block may be cut into so that the SMs
-// have three each (a piece has at least kPieceSteps steps of 64 positions).
-constexpr int kPromptPieces = 444, kPromptMostPieces = 8, kPieceSteps = 8;
+// group), blocks of two tiles there can be, and the most pieces that a block may be cut into (a piece has at
+// least kPieceSteps steps of 64 positions; a call has at most kPromptPieces, three for each SM).
+constexpr int kPromptPieces = 444, kPromptMostPieces = 8, kPieceSteps = 16;
 static_assert(256 + kPromptPieces * 8 <= kPagedHead, "the counts of finished pieces lie in the head");
 inline int prompt_pack(const PagedShape& s, int n_heads) {
   const int group = n_heads / s.kv, pack = group & -group;
@@ -95,17 +95,12 @@ struct PromptPlan {
   size_t total;
 };
 inline PromptPlan prompt_plan(const PagedShape& s, int n_heads, int n_lanes, int n_rows) {
-  const int pack = prompt_pack(s, n_heads);
+  const int pack = prompt_pack(s, n_heads), pieces = s.max_len() / (kPieceSteps * 64);
   PromptPlan w;
   w.blocks = ((long long)n_rows / (256 / pack) + n_lanes) * (n_heads / pack);  // at least the lanes' blocks
-  const long long by_len = s.max_len() / (kPieceSteps * 64), by_sms = kPromptPieces / w.blocks;
-  w.pieces = (int)(by_len < by_sms ? by_len : by_sms);
-  w.pieces = w.pieces < 1 ? 1 : w.pieces > kPromptMostPieces ? kPromptMostPieces : w.pieces;
-  w.total = kPagedHead + (w.pieces > 1 ? (size_t)w.blocks * w.pieces * 2 * 128 * (s.hd + 2) * 4 : 0);
+  w.pieces = pieces < 1 ? 1 : pieces > kPromptMostPieces ? kPromptMostPieces : pieces;
+  w.total = kPagedHead + (w.pieces > 1 ? (size_t)kPromptPieces * 2 * 128 * (s.hd + 2) * 4 : 0);
   return w;
-}
-inline size_t prompt_workspace_most(const PagedShape& s) {
-  return kPagedHead + (s.max_len() >= 2 * kPieceSteps * 64 ? (size_t)kPromptPieces * 2 * 128 * (s.hd + 2) * 4 : 0);
 }
 struct PagedOpsWorkspace {
   size_t count_off, moves_off, list_off, total;

@@ -139,7 +139,7 @@ tl_status tl_paged_workspace_bytes(const tl_paged_desc* desc, int32_t n_heads, i
     return set_error(TL_ERR_UNSUPPORTED, "n_lanes %d > %d lanes per call", n_lanes, tl::kPagedMaxLanes);
   if ((st = check_split(split_rows)) != TL_OK) return st;
   size_t most = tl::paged_workspace_upto(s, n_heads, n_lanes, split_rows);
-  for (const size_t need : {tl::paged_ops_workspace(s).total, tl::prompt_workspace_most(s)})
+  for (const size_t need : {tl::paged_ops_workspace(s).total, tl::prompt_plan(s, n_heads, 1, 1).total})
     if (need > most) most = need;
   *bytes = most;
   return TL_OK;
@@ -219,7 +219,7 @@ tl_status tl_paged_prompt_attn(const tl_paged_desc* desc, tl_paged_cache cache, 
   if ((st = check_scale(&scale, s.hd)) != TL_OK) return st;
   const tl::PromptPlan plan = tl::prompt_plan(s, n_heads, n_lanes, n_rows);
   if ((st = check_workspace(workspace, workspace_bytes, plan.total)) != TL_OK) return st;
-  if (plan.blocks > INT32_MAX / 4)
+  if (plan.blocks > INT32_MAX / 16)
     return set_error(TL_ERR_UNSUPPORTED, "%d rows of %d heads in one call", n_rows, n_heads);
   const tl::PagedPromptArgs a{s, bufs(cache), layer, n_heads, n_lanes, n_rows, q, q_stride, cu_q,
                               kv_len, seqs, scale, out, (uint8_t*)workspace, plan};
