@@ -28,7 +28,7 @@ struct PagedBufs {
 // Splits of one lane's `len` positions: target = the splits a lane should have so that the call
 // fills the GPU (0: splits of `fixed` positions).  Otherwise at least ceil(len / kSplitMost)
 // splits, at most one per kSplitLeast positions, of equal length rounded up to 16 positions (a warp's unit).
-constexpr int kSplitLeast = 128, kSplitMost = 2048;
+constexpr int kSplitLeast = 128, kSplitMost = 1024;
 __host__ __device__ inline int paged_split_rows(int len, int target, int fixed) {
   if (target == 0) return fixed;
   const int fine = (len + kSplitLeast - 1) / kSplitLeast, coarse = (len + kSplitMost - 1) / kSplitMost;
