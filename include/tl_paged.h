@@ -25,7 +25,7 @@
  * bytes zeroed once; the status word is its first).  Calls on one stream may share a workspace,
  * and so may captured graphs that are replayed one after the other; calls that may overlap on
  * the GPU need one each, except tl_paged_append, tl_paged_fork and tl_paged_free, which touch
- * only the status word.
+ * only the status word.  After TL_ERR_DEVICE_TIMEOUT the 4096 bytes are to be zeroed again.
  */
 #ifndef TL_PAGED_H_
 #define TL_PAGED_H_
@@ -95,6 +95,7 @@ TL_API tl_status tl_paged_workspace_bytes(const tl_paged_desc* desc, int32_t n_h
  *   start_pos device int32 [n_lanes]: lane b's row i goes to position start_pos[b] + i
  *   seqs      device int32 [n_lanes] or NULL: the sequence (table row) of each lane; NULL: lane b
  *             is sequence b
+ * No two rows of a call may go to the same position.
  * A row whose sequence or position is out of range, whose page is not in the table, or whose page
  * is held by more than one sequence (refs > 1: tl_paged_reserve gives the writer its own) is not
  * written, and TL_ERR_DEVICE_RANGE is recorded.

@@ -429,7 +429,11 @@ def residual_norm_check(residual, threshold: float, it: int, loops, abort_flags,
 
 def poll_status(cache, stream=None) -> int:
     """Synchronise and return (and clear) the device status of a workspace: a StoreHCache's,
-    a DeltaCache's made with n_lanes, or a workspace tensor of its own (verification, prefill)."""
+    a DeltaCache's made with n_lanes, a PagedCache's, or a workspace tensor of its own (verification, prefill)."""
+    if isinstance(cache, PagedCache):
+        import torch
+        with torch.cuda.device(cache.device):
+            return _load().tl_storeh_poll_status(*cache._tail, _stream(stream))
     if hasattr(cache, "workspace"):
         return _load().tl_storeh_poll_status(cache.workspace.data_ptr(), cache.ws_bytes, _stream(stream))
     return _load().tl_storeh_poll_status(cache.data_ptr(), int(cache.numel()), _stream(stream))
@@ -582,6 +586,8 @@ def _paged_call(cache: PagedCache, fn: str, args, stream) -> None:
     """Calls fn(desc, cache, *args, workspace, its size, stream) with the cache's device current; the stream
     None is that device's current one."""
     c = cache._torch_c
+    if cache._index < 0:
+        raise ValueError(f"the cache is on {cache.device}, not on a GPU")
     if c._cuda_getDevice() != cache._index:
         import torch
         with torch.cuda.device(cache._index):

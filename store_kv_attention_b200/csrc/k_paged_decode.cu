@@ -45,7 +45,7 @@ struct DecodeParams {
   float* acc;  // [lanes][heads][s_max][hd]
   uint32_t* status;
   float scale2;  // scale * log2 e
-  int n_heads, group, head_tiles, n_lanes, s_max, target, fixed;
+  int n_heads, group, head_tiles, n_lanes, s_max, target, rows;
 };
 
 // Positions lane b attends, or -1 for a lane that is out of range.
@@ -118,7 +118,7 @@ __device__ void lane_splits(const DecodeParams& p, int* prefix) {
       if (len < 0) {
         if (blockIdx.x == 0) atomicOr(p.status, kStatusRange);
       } else {
-        n = paged_splits(len, p.target, p.fixed);
+        n = paged_splits(len, p.target, p.rows);
       }
     }
     int incl = n;
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Deco
     const int n_rows = min(16, (kvh + 1) * p.group - h0);  // query heads of the tile
     int seq;
     const int len = lane_len(p, b, &seq);
-    const int per = paged_split_rows(len, p.target, p.fixed);
+    const int per = paged_split_rows(len, p.target, p.rows);
     const int c0 = split * per, c1 = min(len, c0 + per);
     const int units = c1 > c0 ? (c1 - c0 + kUnit - 1) / kUnit : 0;
     const int my_units = units > warp ? (units - warp + kWarps - 1) / kWarps : 0;  // units warp, warp + 4, ...
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const DecodePa
   const int h = blockIdx.x, b = blockIdx.y, t = threadIdx.x;
   int seq;
   const int len = lane_len(p, b, &seq);
-  const int n = len < 0 ? 0 : paged_splits(len, p.target, p.fixed);
+  const int n = len < 0 ? 0 : paged_splits(len, p.target, p.rows);
   if (n <= 1) return;  // a single split wrote the output itself
   const size_t first = ((size_t)b * p.n_heads + h) * p.s_max;
   const float2* ml = reinterpret_cast<const float2*>(p.ml) + first;
@@ -506,7 +506,7 @@ cudaError_t launch_paged_decode(const PagedDecodeArgs& a, cudaStream_t st) {
                  a.n_lanes,
                  a.wl.s_max,
                  a.wl.target,
-                 a.split_rows};
+                 a.wl.rows};
   if (s.hd == 64) return s.dtype == TL_KV_BF16 ? launch_as<64, true>(p, st) : launch_as<64, false>(p, st);
   return s.dtype == TL_KV_BF16 ? launch_as<128, true>(p, st) : launch_as<128, false>(p, st);
 }

@@ -25,22 +25,30 @@ struct PagedBufs {
   int32_t* refs;
 };
 
-// Splits of one lane's `len` positions: target = the splits a lane should have so that the call
-// fills the GPU (0: splits of `fixed` positions).  Otherwise at least ceil(len / kSplitMost)
-// splits, at most one per kSplitLeast positions, of equal length rounded up to 16 positions (a warp's unit).
-constexpr int kSplitLeast = 128, kSplitMost = 1024;
-__host__ __device__ inline int paged_split_rows(int len, int target, int fixed) {
-  if (target == 0) return fixed;
-  const int fine = (len + kSplitLeast - 1) / kSplitLeast, coarse = (len + kSplitMost - 1) / kSplitMost;
+// Splits of one lane's `len` positions.  target 0: splits of `rows` positions.  Otherwise target = the splits a
+// lane should have so that the call fills the GPU, `rows` = the most positions of a split: as many splits as the
+// two ask for, at most one per kSplitLeast positions, of equal length rounded up to 16 positions (a warp's unit).
+constexpr int kSplitLeast = 128;
+__host__ __device__ inline int paged_split_rows(int len, int target, int rows) {
+  if (target == 0) return rows;
+  const int fine = (len + kSplitLeast - 1) / kSplitLeast, coarse = (len + rows - 1) / rows;
   int n = fine < target ? fine : target;
   n = n > coarse ? n : coarse;
   n = n > 1 ? n : 1;
-  const int rows = (len + n - 1) / n;
-  return rows <= 16 ? 16 : (rows + 15) / 16 * 16;
+  const int each = (len + n - 1) / n;
+  return each <= 16 ? 16 : (each + 15) / 16 * 16;
 }
-__host__ __device__ inline int paged_splits(int len, int target, int fixed) {
-  const int rows = paged_split_rows(len, target, fixed);
-  return len <= rows ? 1 : (len + rows - 1) / rows;
+__host__ __device__ inline int paged_splits(int len, int target, int rows) {
+  const int each = paged_split_rows(len, target, rows);
+  return len <= each ? 1 : (len + each - 1) / each;
+}
+// The most positions of a split: 1024 (32 lanes of 4097: 178 us a call, 186 at 2048, 192 at 512; 48 lanes of up to
+// 8192: 142, 148, 151), or more where a call's lanes, were they all as long as the table allows, would have more
+// than 2^18 partial results.
+constexpr int kSplitMost = 1024, kMostParts = 1 << 18;
+inline int paged_split_most(int max_len, int n_heads, int n_lanes) {
+  const long long parts = (long long)n_lanes * n_heads * ((max_len + kSplitMost - 1) / kSplitMost);
+  return kSplitMost * (int)((parts + kMostParts - 1) / kMostParts);
 }
 
 // Workspace: a head that is zero between calls (status word | work queue of the prompt attention |
@@ -50,7 +58,7 @@ __host__ __device__ inline int paged_splits(int len, int target, int fixed) {
 constexpr int kPagedQueueOff = 128, kPagedHead = 4096;
 struct PagedWorkspace {
   size_t ml_off, acc_off, total;  // decode
-  int s_max, target;              // splits a lane can have; paged_split_rows' target
+  int s_max, target, rows;        // splits a lane can have; paged_split_rows' arguments
 };
 // K/V heads times tiles of 16 query heads: the CTAs that one split of one lane takes.
 inline int paged_tiles(const PagedShape& s, int n_heads) { return s.kv * ((n_heads / s.kv + 15) / 16); }
@@ -58,26 +66,29 @@ constexpr int kPagedSlots = 296;  // two CTAs on each of the 148 SMs
 inline PagedWorkspace paged_workspace(const PagedShape& s, int n_heads, int n_lanes, int split_rows) {
   PagedWorkspace w;
   const int pairs = n_lanes * paged_tiles(s, n_heads), len = s.max_len();
-  const int fine = (len + kSplitLeast - 1) / kSplitLeast, coarse = (len + kSplitMost - 1) / kSplitMost;
   w.target = split_rows ? 0 : (kPagedSlots + pairs - 1) / pairs;
+  w.rows = split_rows ? split_rows : paged_split_most(len, n_heads, n_lanes);
+  const int fine = (len + kSplitLeast - 1) / kSplitLeast, coarse = (len + w.rows - 1) / w.rows;
   w.s_max = w.target < fine ? w.target : fine;
   if (w.s_max < coarse) w.s_max = coarse;
-  if (split_rows) w.s_max = (len + split_rows - 1) / split_rows;
   const size_t parts = (size_t)n_lanes * n_heads * w.s_max;
   w.ml_off = kPagedHead;
   w.acc_off = align256(w.ml_off + parts * 8);
   w.total = align256(w.acc_off + parts * s.hd * 4);
   return w;
 }
-// Enough for every call of up to n_lanes lanes: with fewer lanes a lane has more splits, but
-// n * ceil(slots / (n * tiles)) never passes slots / tiles + n.
+// Enough for every call of up to n_lanes lanes.  With fewer lanes a lane has more splits, but
+// n * ceil(slots / (n * tiles)) never passes slots / tiles + n, nor n * heads * ceil(len / most) the larger of
+// kMostParts + n * heads and the parts of 1024 positions.
 inline size_t paged_workspace_upto(const PagedShape& s, int n_heads, int n_lanes, int split_rows) {
-  const size_t fine = (s.max_len() + kSplitLeast - 1) / kSplitLeast, coarse = (s.max_len() + kSplitMost - 1) / kSplitMost;
-  size_t lane_splits = kPagedSlots / paged_tiles(s, n_heads) + 1 + (size_t)n_lanes;
-  if (lane_splits > n_lanes * fine) lane_splits = n_lanes * fine;
-  if (lane_splits < n_lanes * coarse) lane_splits = n_lanes * coarse;
-  if (split_rows) lane_splits = n_lanes * (size_t)((s.max_len() + split_rows - 1) / split_rows);
-  const size_t parts = lane_splits * n_heads;
+  const size_t len = s.max_len(), lanes = n_lanes;
+  const size_t fine = lanes * ((len + kSplitLeast - 1) / kSplitLeast) * n_heads;
+  size_t coarse = lanes * ((len + kSplitMost - 1) / kSplitMost) * n_heads;
+  if (coarse > kMostParts + lanes * n_heads) coarse = kMostParts + lanes * n_heads;
+  size_t parts = (kPagedSlots / paged_tiles(s, n_heads) + 1 + lanes) * n_heads;
+  if (parts > fine) parts = fine;
+  if (parts < coarse) parts = coarse;
+  if (split_rows) parts = lanes * ((len + split_rows - 1) / split_rows) * n_heads;
   return align256(align256(kPagedHead + parts * 8) + parts * s.hd * 4);
 }
 // Prompt attention: heads packed into a tile's rows (the largest power of two up to 128 that divides the
@@ -117,7 +128,7 @@ inline PagedOpsWorkspace paged_ops_workspace(const PagedShape& s) {
 struct PagedDecodeArgs {
   PagedShape s;
   PagedBufs c;
-  int layer, n_heads, n_lanes, split_rows;
+  int layer, n_heads, n_lanes;
   const void* q;
   int64_t q_stride;
   const int32_t* kv_len;

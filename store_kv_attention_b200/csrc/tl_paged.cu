@@ -192,7 +192,7 @@ tl_status tl_paged_attn_decode(const tl_paged_desc* desc, tl_paged_cache cache, 
   if ((st = check_workspace(workspace, workspace_bytes, wl.total)) != TL_OK) return st;
   if ((int64_t)n_lanes * wl.s_max * tl::paged_tiles(s, n_heads) > INT32_MAX)
     return set_error(TL_ERR_UNSUPPORTED, "%d lanes of %d splits in one call", n_lanes, wl.s_max);
-  const tl::PagedDecodeArgs a{s, bufs(cache), layer, n_heads, n_lanes, split_rows, q, q_stride, kv_len,
+  const tl::PagedDecodeArgs a{s, bufs(cache), layer, n_heads, n_lanes, q, q_stride, kv_len,
                               seqs, scale, out, (uint8_t*)workspace, wl};
   cudaError_t e = tl::launch_paged_decode(a, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_error(e, "tl_paged_attn_decode launch");

@@ -359,6 +359,50 @@ def test_prompt_row_equals_decode_of_the_same_position(tl):
     rig.check_decode(0, q[[499, 576]], out[[499, 576]])
 
 
+def test_a_thousand_lanes(tl):
+    """As many lanes as a call may have, some empty, in a table that would hold 2^22 positions each."""
+    rng = np.random.default_rng(5)
+    new = rng.integers(0, 4, 1024)
+    total = (new + rng.integers(0, 60, 1024)).tolist()
+    rig = Rig(tl, total, kv=1, group=2, hd=64, page=16, dtype=FP16, layers=1, n_lanes=1024, seqs=rng.permutation(1024).tolist())
+    wide = tl.PagedDesc(1, rig.cache.desc.n_pages, 16, 1, 64, 1025, 262144, tl.TL_KV_FP16)
+    table = torch.full((1025, 262144), -1, dtype=torch.int32, device="cuda")
+    table[:, :rig.table.shape[1]] = torch.from_numpy(rig.table[:1025]).cuda()
+    rig.cache = tl.PagedCache(wide, 2, 1024, k=rig.cache.k, v=rig.cache.v, table=table, refs=rig.cache.refs)
+    cu = np.cumsum([0] + new.tolist()).tolist()
+    q, tok = rig.queries(cu[-1]), rig.queries(1024)
+    out, o1 = torch.full_like(q, float("nan")), torch.full_like(tok, float("nan"))
+    tl.paged_prompt_attn(rig.cache, 0, q, _i32(cu), _i32(total), out, seqs=_i32(rig.seqs))
+    tl.paged_attn_decode(rig.cache, 0, tok, _i32(total), o1, seqs=_i32(rig.seqs))
+    rig.ok()
+    rig.check_prompt(0, q, cu, out)
+    rig.check_decode(0, tok, o1)
+
+
+def test_two_streams_with_a_workspace_each(tl):
+    """Calls that overlap on the GPU, each on a workspace of its own over the same pool: the bits of calls alone."""
+    lens = [3000, 500, 1200]
+    rig = Rig(tl, lens, kv=2, group=4, hd=128, page=16, dtype=BF16, layers=1)
+    c = rig.cache
+    other = tl.PagedCache(c.desc, rig.heads, 3, k=c.k, v=c.v, table=c.table, refs=c.refs)
+    cu, n, kv = _i32([0, 200, 300, 700]), 700, _i32(lens)
+    q = rig.queries(n)
+    want, w1 = torch.empty_like(q), torch.empty_like(q[:3])
+    tl.paged_prompt_attn(c, 0, q, cu, kv, want)
+    tl.paged_attn_decode(c, 0, q[:3], kv, w1)
+    outs = [(torch.empty_like(q), torch.empty_like(q[:3])) for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for cache, (a, b), st in zip((c, other), outs, streams):
+            tl.paged_prompt_attn(cache, 0, q, cu, kv, a, stream=st)
+            tl.paged_attn_decode(cache, 0, q[:3], kv, b, stream=st)
+    torch.cuda.synchronize()
+    for a, b in outs:
+        assert torch.equal(a, want) and torch.equal(b, w1)
+    assert tl.poll_status(c) == tl.TL_OK and tl.poll_status(other) == tl.TL_OK
+
+
 # ---------------------------------------------------------------------------------------- pages
 class Twin:
     """A cache beside the oracle's list walks: each operation on both, then everything compared."""

@@ -39,7 +39,7 @@ def test_desc_validation(tl, kw, status):
     assert e.value.status == status
 
 
-@pytest.mark.parametrize("max_pages", [1, 20, 4096])
+@pytest.mark.parametrize("max_pages", [1, 20, 4096, 262144])
 @pytest.mark.parametrize("heads", [4, 12, 128])
 def test_workspace_covers_every_smaller_call(tl, max_pages, heads):
     """The workspace of n lanes is enough for every call of fewer: the launch's own need, from its refusal."""
@@ -139,6 +139,8 @@ def test_binding_checks_tensors(tl):
         tl.paged_fork(c, lens, lens[:2], lens)
     with pytest.raises(ValueError):
         tl.PagedCache(d, n_heads=8, n_lanes=4, k=c.k[:, :10])
+    with pytest.raises(ValueError):
+        tl.paged_attn_decode(c, 0, q, lens, out)                # a cache on the host
 
 
 def test_oracle_attend_against_torch():
