@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Deco
   uint8_t* ring = smem + warp * (kRing / kWarps);
   const uint32_t ring_addr = ptx::smem_addr(ring);
   const PagedShape& s = p.s;
-  const int tiles = s.kv * p.head_tiles;
+  const int tiles = s.kv * p.head_tiles, log_page = 31 - __clz(s.page);
   const int items = prefix[p.n_lanes] * tiles;  // at most 1024 lanes x s_max splits x tiles: checked on the host
 
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Deco
       const int i = i0 + lane;
       pages = -1;
       if (i < my_units) {
-        const int pg = row[(c0 + (warp + i * kWarps) * kUnit) / s.page];
+        const int pg = row[(c0 + (warp + i * kWarps) * kUnit) >> log_page];
         if (pg >= 0 && pg < s.n_pages)
           pages = pg;
         else
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Deco
         if ((i & 31) == 0) load_pages(i);
         const int pg = __shfl_sync(0xffffffffu, pages, i & 31);
         const int pos = c0 + (warp + i * kWarps) * kUnit;
-        const size_t at = ((size_t)(pg < 0 ? 0 : pg) * s.kv + kvh) * s.block_elems() + (size_t)(pos % s.page) * HD;
+        const size_t at = ((size_t)(pg < 0 ? 0 : pg) * s.kv + kvh) * s.block_elems() + (size_t)(pos & (s.page - 1)) * HD;
         const uint32_t dst = ring_addr + (i % kStages) * kStageBytes;
 #pragma unroll
         for (int k = 0; k < kCopies; ++k) {
