@@ -33,20 +33,17 @@ __global__ void __launch_bounds__(kAppendThreads)
                         const int32_t* start_pos, const int32_t* seqs, int n_lanes, uint32_t* status) {
   ptx::pdl_wait();
   ptx::pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int chunks = s.kv * s.hd / 8, parts = (chunks + kPart - 1) / kPart;
-  const int per_head = s.hd / 8;
-  const long long units = (long long)n_rows * parts * 2;
-  const long long step = (long long)gridDim.x * (kAppendThreads / 32);
+  const int lane = threadIdx.x & 31, part = blockIdx.y >> 1;
+  const bool is_v = blockIdx.y & 1;
+  const int chunks = s.kv * s.hd / 8, log_page = 31 - __clz(s.page), log_head = s.hd == 64 ? 3 : 4;  // 16-byte chunks
   int first = 0, last = n_rows;
   if (cu_rows) {
-    first = cu_rows[0];
-    last = cu_rows[n_lanes];
+    first = max(0, cu_rows[0]);
+    last = min(n_rows, cu_rows[n_lanes]);
   }
-  for (long long u = (long long)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5); u < units; u += step) {
-    const bool is_v = u & 1;
-    const int part = (int)((u >> 1) % parts), r = (int)((u >> 1) / parts);
-    if (r < first || r >= last) continue;
+  const int step = gridDim.x * (kAppendThreads / 32);
+  for (long long at_row = (long long)first + blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5); at_row < last; at_row += step) {
+    const int r = (int)at_row;
     // the row's values are on their way while its place is looked up
     const uint4* src = reinterpret_cast<const uint4*>(is_v ? v_rows + r * v_stride : k_rows + r * k_stride);
     uint4 x[4];
@@ -60,18 +57,18 @@ __global__ void __launch_bounds__(kAppendThreads)
     const long long pos = (long long)start_pos[b] + (cu_rows ? r - cu_rows[b] : 0);
     bool ok = seq >= 0 && seq < s.max_seqs && pos >= 0 && pos < s.max_len();
     int page = -1;
-    if (ok) page = c.table[(size_t)seq * s.max_pages + (int)(pos / s.page)];
+    if (ok) page = c.table[(size_t)seq * s.max_pages + (int)(pos >> log_page)];
     ok = ok && page >= 0 && page < s.n_pages;
     if (ok && c.refs) ok = c.refs[page] <= 1;
     if (!ok) {
       if (lane == 0) atomicOr(status, kStatusRange);
       continue;
     }
-    uint16_t* dst = (is_v ? c.v : c.k) + layer_off + (size_t)page * s.page_elems() + (size_t)(pos % s.page) * s.hd;
+    uint16_t* dst = (is_v ? c.v : c.k) + layer_off + (size_t)page * s.page_elems() + (size_t)((int)pos & (s.page - 1)) * s.hd;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int at = part * kPart + i * 32 + lane;
-      if (at < chunks) *reinterpret_cast<uint4*>(dst + (size_t)(at / per_head) * s.block_elems() + (at % per_head) * 8) = x[i];
+      if (at < chunks) *reinterpret_cast<uint4*>(dst + (size_t)(at >> log_head) * s.block_elems() + (at & ((1 << log_head) - 1)) * 8) = x[i];
     }
   }
 }
@@ -82,14 +79,14 @@ cudaError_t launch_paged_append(const PagedShape& s, const PagedBufs& c, int lay
                                 const void* v_rows, int64_t v_stride, int n_rows, const int32_t* cu_rows,
                                 const int32_t* start_pos, const int32_t* seqs, int n_lanes, uint32_t* status,
                                 cudaStream_t st) {
-  const long long units = (long long)n_rows * ((s.kv * s.hd / 8 + kPart - 1) / kPart) * 2;
-  const long long blocks = (units + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
+  const int parts = (s.kv * s.hd / 8 + kPart - 1) / kPart;
+  const long long blocks = ((long long)n_rows + kAppendThreads / 32 - 1) / (kAppendThreads / 32), most = (148 * 8 + 2 * parts - 1) / (2 * parts);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = st;
-  cfg.gridDim = dim3((unsigned)(blocks < 148 * 8 ? blocks : 148 * 8));
+  cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most), 2 * parts);
   cfg.blockDim = dim3(kAppendThreads);
   cudaError_t e = cudaLaunchKernelEx(&cfg, paged_append_kernel, s, c, (size_t)layer * s.layer_elems(),
                                      (const uint16_t*)k_rows, k_stride, (const uint16_t*)v_rows, v_stride, n_rows,
