@@ -59,34 +59,36 @@ __device__ T block_scan(T x, T* total) {
   return before + incl - x;
 }
 
-// Walks refs in page order, 16 pages a thread, and calls f(page, refs, rank) for every page with
-// (refs > 0) == live in [0, end), rank counting them; stops behind the first `most`.  Returns how
-// many there are (at least `most`, when it stopped early).
-template <typename F>
-__device__ int walk_pages(const int32_t* refs, int end, bool live, int most, F f) {
+// The counts of 16 pages from p0 on (a multiple of 4; refs is 256-byte aligned); -1 from `end` on.
+__device__ __forceinline__ void load_refs(const int32_t* refs, int p0, int end, int* r) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    if (p0 + i + 3 < end) {
+      const int4 x = *reinterpret_cast<const int4*>(refs + p0 + i);
+      r[i] = x.x, r[i + 1] = x.y, r[i + 2] = x.z, r[i + 3] = x.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r[i + k] = p0 + i + k < end ? refs[p0 + i + k] : -1;
+    }
+  }
+}
+
+// The first `most` free pages, lowest first, into list; returns how many pages are free, counted until there are
+// `most`.
+__device__ int free_pages_of(const int32_t* refs, int n_pages, int most, int32_t* list) {
   int seen = 0;
-  for (int base = 0; base < end && seen < most; base += kPlanThreads * 16) {
+  for (int base = 0; base < n_pages && seen < most; base += kPlanThreads * 16) {
     const int p0 = base + threadIdx.x * 16;
     int r[16], n = 0;
+    load_refs(refs, p0, n_pages, r);
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {  // refs is 256-byte aligned
-      if (p0 + i + 3 < end) {
-        const int4 x = *reinterpret_cast<const int4*>(refs + p0 + i);
-        r[i] = x.x, r[i + 1] = x.y, r[i + 2] = x.z, r[i + 3] = x.w;
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (p0 + i + k < end) r[i + k] = refs[p0 + i + k];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) n += p0 + i < end && (r[i] > 0) == live;
+    for (int i = 0; i < 16; ++i) n += p0 + i < n_pages && r[i] <= 0;
     int total;
     int rank = seen + block_scan(n, &total);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      if (p0 + i < end && (r[i] > 0) == live) {
-        if (rank < most) f(p0 + i, r[i], rank);
+      if (p0 + i < n_pages && r[i] <= 0) {
+        if (rank < most) list[rank] = p0 + i;
         ++rank;
       }
     seen += total;
@@ -292,8 +294,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     needed += __syncthreads_count(i < total && needs(find(i), i, &was));
   }
   // the lowest free pages
-  const int free_pages =
-      walk_pages(c.refs, s.n_pages, false, needed, [&](int p, int, int rank) { plan.list[rank] = p; });
+  const int free_pages = free_pages_of(c.refs, s.n_pages, needed, plan.list);
   // too few: the first sequence whose need, with those before it, passes them
   if (free_pages < needed) {
     int before = 0;
@@ -350,23 +351,41 @@ __global__ void __launch_bounds__(kPlanThreads)
     paged_compact_plan_kernel(PagedShape s, PagedBufs c, Plan plan, int32_t* n_live) {
   ptx::pdl_wait();
   ptx::pdl_trigger();
-  int live, mine = 0;
-  for (int p = threadIdx.x; p < s.n_pages; p += kPlanThreads) mine += c.refs[p] > 0;
+  int live, mine = 0, r[16];
+  for (int base = 0; base < s.n_pages; base += kPlanThreads * 16) {
+    load_refs(c.refs, base + threadIdx.x * 16, s.n_pages, r);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mine += r[i] > 0;
+  }
   block_scan(mine, &live);
-  const int holes = walk_pages(c.refs, live, false, s.n_pages, [&](int p, int, int rank) { plan.moves[rank].y = p; });
-  // live pages at or above `live`: as many as there are holes below it
-  for (int p = live + threadIdx.x; p < s.n_pages; p += kPlanThreads) plan.list[p] = -1;
-  __syncthreads();
-  const int below = live - holes;
-  walk_pages(c.refs, s.n_pages, true, s.n_pages, [&](int p, int r, int rank) {
-    if (p < live) return;
-    const int to = plan.moves[rank - below].y;
-    plan.moves[rank - below].x = p;
-    plan.list[p] = to;
-  });
+  // free pages below `live` and pages in use from there on: as many of the one as of the other
+  int holes = 0, movers = 0;
+  for (int base = 0; base < s.n_pages; base += kPlanThreads * 16) {
+    const int p0 = base + threadIdx.x * 16;
+    if (s.n_pages > kPlanThreads * 16) load_refs(c.refs, p0, s.n_pages, r);  // else they are still there
+    int h = 0, m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      h += p0 + i < live && r[i] <= 0;
+      m += p0 + i >= live && r[i] > 0;
+    }
+    long long sum;
+    const long long at = block_scan<long long>((long long)h | (long long)m << 32, &sum);
+    int hole = holes + (int)(at & 0xffffffff), mover = movers + (int)(at >> 32);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int p = p0 + i;
+      if (p < live && r[i] <= 0) plan.moves[hole++].y = p;
+      if (p >= live && r[i] > 0) plan.moves[mover++].x = p;
+      if (p >= live && p < s.n_pages && r[i] <= 0) plan.list[p] = -1;  // for a table that names a page it does not hold
+    }
+    holes += (int)(sum & 0xffffffff);
+    movers += (int)(sum >> 32);
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < holes; i += kPlanThreads) {
     const int2 m = plan.moves[i];
+    plan.list[m.x] = m.y;
     c.refs[m.y] = c.refs[m.x];
     c.refs[m.x] = 0;
   }

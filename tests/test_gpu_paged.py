@@ -482,6 +482,20 @@ def test_pages_at_size(tl, n_pages, max_pages):
     t.do("compact")
 
 
+def test_pages_with_counts_that_are_not_the_tables(tl):
+    """A table entered by hand without counts, then freed (counts below 0) and compacted: no page is lost or copied
+    to where there is none, and what is not counted is free."""
+    t = Twin(tl, n_pages=40, page=16, max_seqs=4, max_pages=6)
+    t.do("reserve", [0], [0], [40])
+    t.cache.table[1, :3] = _i32([30, 20, 39])
+    tl.paged_free(t.cache, _i32([1]))
+    assert t.cache.refs[[20, 30, 39]].tolist() == [-1] * 3
+    tl.paged_compact(t.cache)
+    tl.paged_reserve(t.cache, _i32([2]), _i32([0]), _i32([96]))
+    assert tl.poll_status(t.cache) == tl.TL_OK
+    assert t.cache.table[0].tolist() == [0, 1, 2, -1, -1, -1] and t.cache.table[2].tolist() == [3, 4, 5, 6, 7, 8]
+
+
 def test_reserve_a_thousand_sequences(tl):
     t = Twin(tl, n_pages=1500, page=16, max_seqs=1030, max_pages=2, layers=1, kv=1)
     order = np.random.default_rng(0).permutation(1030)[:1024].tolist()
