@@ -12,7 +12,10 @@
 // the end in shared memory.  The products are m16n8k16 matrix instructions: 16 query heads x 16
 // positions; at 16 rows per K/V byte the matrix work is a few percent of their rate, and their
 // operands come from registers, without the tensor-memory round trips of tcgen05 that bound
-// the store-h streaming kernel.
+// the store-h streaming kernel.  Measured: 32 lanes of 4097 positions, 16 heads x 128, 172 us a launch, 6.2
+// TB/s (0.96 of a copy's bandwidth); 48 lanes of 0 to 8192, 32 heads over 8, 139 us, 5.9 TB/s; one lane of 60001
+// over 2 K/V heads 16.5 us, of which 8 are the stream and 4 the loads of its length, its pages and its first rows,
+// one behind the other.
 //
 // Precision: scores, statistics and sums in FP32; p is rounded to the cache's type for the second
 // product (half a step, 2^-11 or 2^-8 relative, the rounding that the output itself has), its sum is
