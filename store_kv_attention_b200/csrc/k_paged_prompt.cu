@@ -20,13 +20,13 @@
 //             when there is nothing to wait for, pass behind the products of the other).  Each tile has
 //             two S buffers of 64 columns: S_t(u+2) is issued behind P_t(u) V(u), so that the next S
 //             is there while a tile's softmax runs and the tensor pipe has products meanwhile
-//   9, 10     take work and load by TMA, page by page (a page of one K/V head is one box per 64 values):
-//             Q and K / V.  A slot of the ring holds what one issue of products takes, K(u+2) and V(u).
+//   9, 10     load by TMA, page by page (a page of one K/V head is one box per 64 values): Q and K / V.  A slot of the ring holds what one issue of products takes, K(u+2) and V(u).
 //             (Two warps: a box costs some 50 clocks of issue, a step of 16-position pages 16 boxes.)
-//             Warp 9 also cleans the V steps that hold positions not every row attends, before it
-//             takes the next work: rows past the cache's end are zeroed (their memory may hold
-//             anything) and values that are not finite are taken out (0 x inf would reach the rows that
-//             do not attend them) and given back at the end to the rows that do
+//             Warp 9 also cleans the V steps that hold positions not every row attends: rows past the
+//             cache's end are zeroed (their memory may hold anything) and values that are not finite are
+//             taken out (0 x inf would reach the rows that do not attend them) and given back at the end
+//             to the rows that do
+//   12        takes work (a job: a block or a piece of one) and looks its lane's pages over, 3 us ahead
 // O is rescaled only when a row's maximum has grown by more than 2^8 in the exponent since the last
 // time: the base of the exponents is a free choice (P then reaches 2^8 and its sum 2^8 times the
 // positions, far inside FP32), and the rescale, a round trip of O through registers, becomes rare.
@@ -52,10 +52,11 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kPromptThreads = 384;
+constexpr int kPromptThreads = 512;
 constexpr int kTile = 128;                // query rows of a tile
 constexpr int kStep = 64;                 // positions of a step
 constexpr int kSms = 148;
+constexpr int kAhead = 8;                 // turns before a job's last that the next one is taken
 constexpr long long kPWait = 4000000000ll;  // SM clocks
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.0f;  // growth of the maximum, in powers of two, that O is rescaled for
@@ -168,10 +169,9 @@ struct Joint {
 };
 
 // The end of a tile's job, by the threads of its rows: O / l into the output, or the piece's part into the
-// workspace and, by the last piece, the parts joined.  (A function of its own, so that its registers are not
-// the softmax loop's.)  False: a wait gave up.
+// workspace and, by the last piece, the parts joined.  False: a wait gave up.
 template <int HD, bool BF16>
-__device__ __noinline__ bool finish_rows(const PromptParams& p, const CUtensorMap* tmO, const Job& job, int t,
+__device__ __forceinline__ bool finish_rows(const PromptParams& p, const CUtensorMap* tmO, const Job& job, int t,
                                          int log_pack, uint32_t to, uint32_t stage, float m, float l, Joint* joint,
                                          int& parts, volatile int* abort) {
   constexpr int kPartFloats = kTile * (HD + 2);
@@ -353,6 +353,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   __shared__ uint64_t q_full, q_empty, full[kSlots], empty[kSlots], clean[kSlots];
   __shared__ uint64_t s_full[2][2], p_full[2][2], o_done[2][2], job_full[2], job_empty[2], fin[2];
   __shared__ uint32_t tmem_base;
+  __shared__ uint64_t want;
   __shared__ int abort_flag;
   __shared__ Joint joint_mem;
   Joint* joint = &joint_mem;
@@ -366,6 +367,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const int subs = p.n_heads / p.pack, tq = kTile / p.pack;
   if (threadIdx.x == 0) {
     mbar_init(&q_full, 1);
+    mbar_init(&want, 1);
     mbar_init(&q_empty, 2);
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&full[i], 2);   // K's and V's loads
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&joint->done[t], 128);
       mbar_init(&joint->said[t], 1);
       mbar_init(&job_full[t], 1);
-      mbar_init(&job_empty[t], 11);  // warps that read a job
+      mbar_init(&job_empty[t], 12);  // warps that read a job
     }
     abort_flag = 0;
     mbar_fence_init();
@@ -439,7 +441,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     return true;
   };
 
+  // Registers: 512 x 128 at launch = 256 x 184 (softmax: a thread holds a row of S) + 256 x 72.
   if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     // ------------------------------------------------------------ softmax of tile t, row r
     const int t = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -536,274 +540,281 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (lane == 0) mbar_arrive(&job_empty[nj & 1]);
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the outputs are written
-  } else if (warp == 8 || warp == 11) {
-    // ------------------------------------------------------------ products of tile t
-    const int t = warp == 11;
-    bool good = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (good) good = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_p, kPWait));
-      return good;
-    };
-    const uint64_t q_desc = sdesc_sw128(smem_addr(qs + t * Smem::kQ), 16, 1024);
-    const uint64_t k_desc = sdesc_sw128(smem_addr(ks), 16, 1024), v_desc = sdesc_sw128(smem_addr(vs), kStep * 128, 1024);
-    const uint32_t ts = tbase + t * 128, to = tbase + 256 + t * HD;
-    int at = 0, c = 0;         // slots, and steps of this tile, before this job
-    uint32_t clean_phase = 0;  // one bit per slot
-    for (int nj = 0; good; ++nj) {
-      if (!wait(&job_full[nj & 1], (nj >> 1) & 1)) break;
-      const Job& job = jobs[nj & 1];
-      if (job.lane < 0) break;
-      const int n = job.n, nt = job.n_t[t], dirty_from = job.dirty_from;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&job_empty[nj & 1]);
-      if (n == 0) continue;
-      if (!wait(&q_full, nj & 1)) break;
-      // turn w: O_t += P_t(w - 2) V(w - 2), then S_t(w) = Q_t K(w)^T; both operands lie in slot at + w
-      for (int w = 0; w < n + 2; ++w) {
-        const int slot = (at + w) % kSlots, u = w - 2;
-        if (!wait(&full[slot], ((at + w) / kSlots) & 1)) break;
-        if (u >= dirty_from && u >= 0) {
-          if (!wait(&clean[slot], (clean_phase >> slot) & 1)) break;
-          clean_phase ^= 1u << slot;
-        }
-        const bool pv = u >= 0 && u < nt, qk = w < nt;
-        const int buf = (c + w) & 1;  // of step w and of step u
-        if (pv && !wait(&p_full[t][buf], ((c + u) >> 1) & 1)) break;
-        tc_fence_after();
-        if (elect_one()) {
-          if (pv) {
-            const uint64_t b = v_desc + (uint64_t)((slot * Smem::kKv) >> 4);
-#pragma unroll
-            for (int k = 0; k < kStep / 16; ++k)
-              mma_ts(to, ts + buf * kStep + k * 8, b + (uint64_t)((k * 2048) >> 4), kIdO, (u | k) != 0);
-            mma_commit(&o_done[t][buf]);
-          }
-          if (qk) {
-            const uint64_t b = k_desc + (uint64_t)((slot * Smem::kKv) >> 4);
-#pragma unroll
-            for (int k = 0; k < HD / 16; ++k)
-              mma_ss(ts + buf * kStep, q_desc + (uint64_t)(((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4),
-                     b + (uint64_t)(((k / 4) * (kStep * 128) + (k % 4) * 32) >> 4), kIdS, k != 0);
-            mma_commit(&s_full[t][buf]);
-          }
-          // the slot (after the last scores the queries too) is free once these products are done; at once
-          // where this tile attends neither
-          if (pv || qk)
-            mma_commit(&empty[slot]);
-          else
-            mbar_arrive(&empty[slot]);
-          if (w == n - 1) {
-            if (qk)
-              mma_commit(&q_empty);
-            else
-              mbar_arrive(&q_empty);
-          }
-        }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 8 || warp == 11) {
+      // ------------------------------------------------------------ products of tile t
+      const int t = warp == 11;
+      bool good = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (good) good = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_p, kPWait));
+        return good;
+      };
+      const uint64_t q_desc = sdesc_sw128(smem_addr(qs + t * Smem::kQ), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_addr(ks), 16, 1024), v_desc = sdesc_sw128(smem_addr(vs), kStep * 128, 1024);
+      const uint32_t ts = tbase + t * 128, to = tbase + 256 + t * HD;
+      int at = 0, c = 0;         // slots, and steps of this tile, before this job
+      uint32_t clean_phase = 0;  // one bit per slot
+      for (int nj = 0; good; ++nj) {
+        if (!wait(&job_full[nj & 1], (nj >> 1) & 1)) break;
+        const Job& job = jobs[nj & 1];
+        if (job.lane < 0) break;
+        const int n = job.n, nt = job.n_t[t], dirty_from = job.dirty_from;
         __syncwarp();
-        issued = true;
-      }
-      at += n + 2;
-      c += nt;
-    }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ work and loads
-    // the blocks of 2 x tq tokens of 32 lanes at a time; a lane whose rows are out of range has none
-    auto blocks_of = [&](int b, bool note) {
-      if (b >= p.n_lanes) return 0;
-      const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
-      if (q0 >= 0 && q1 <= p.n_rows && q1 >= q0) return (q1 - q0 + 2 * tq - 1) / (2 * tq);
-      if (note) atomicOr(p.status, kStatusRange);
-      return 0;
-    };
-    int blocks = 0, longest = 0;
-    for (int base = 0; base < p.n_lanes; base += 32) {
-      blocks += __reduce_add_sync(0xffffffffu, blocks_of(base + lane, blockIdx.x == 0));
-      if (base + lane < p.n_lanes) longest = max(longest, p.kv_len[base + lane]);
-    }
-    longest = __reduce_max_sync(0xffffffffu, longest);
-    int scan_base = 0, scan_done = 0;  // items only grow: the scan for a lane goes on where the last one stopped
-    // Blocks beyond the last full round over the CTAs are cut into `cut` pieces (a short one into fewer), so that
-    // they take less than a round of their own: the least of rounds x (piece + what a piece costs besides).  Not
-    // where most blocks are too short for it: every piece that there is not is work taken in vain.
-    const int sms = gridDim.x, whole = blocks * subs / sms * sms, rest = blocks * subs - whole;
-    int cut = 1;
-    float best = 1.0f;
-    for (int r = 1; r < 4 && rest > 0; ++r) {
-      const int c = min(min(p.pieces, longest / (2 * kPieceSteps * kStep)), min(r * sms, kPromptPieces) / rest);
-      const float cost = (float)((rest * c + sms - 1) / sms) * (1.0f / (float)c + 0.05f);
-      if (c > 1 && cost < best) {
-        cut = c;
-        best = cost;
-      }
-    }
-    const int items = whole + rest * cut;
-    // Cleans the next V steps of a job that need it, up to step `end`; `first` is the job's first slot.  (This
-    // warp waited for the slots to be free, so it knows which phase of their loads it waits for.)
-    constexpr uint32_t kExp = BF16 ? 0x7f807f80u : 0x7c007c00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
-    int dirty_next = 0;
-    auto clean_steps = [&](Job& job, int first, int end) {
-      const int every = job.kv - job.n_q + job.tok0;  // the last position that every row attends
-      for (; dirty_next < end; ++dirty_next) {
-        const int i = first + dirty_next + 2, slot = i % kSlots;
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], (i / kSlots) & 1, abort_p, kPWait))) return false;
-        uint8_t* tile = vs + slot * Smem::kKv;
-        const int pos = (job.u0 + dirty_next) * kStep, end_row = job.kv - pos;  // the first row to zero
-        bool found = false;
-#pragma unroll 4
-        for (int r = max(0, every + 1 - pos) + (lane >> 3); r < kStep; r += 4) {
+        if (lane == 0) mbar_arrive(&job_empty[nj & 1]);
+        if (n == 0) continue;
+        if (!wait(&q_full, nj & 1)) break;
+        // turn w: O_t += P_t(w - 2) V(w - 2), then S_t(w) = Q_t K(w)^T; both operands lie in slot at + w
+        for (int w = 0; w < n + 2; ++w) {
+          const int slot = (at + w) % kSlots, u = w - 2;
+          if (!wait(&full[slot], ((at + w) / kSlots) & 1)) break;
+          if (u >= dirty_from && u >= 0) {
+            if (!wait(&clean[slot], (clean_phase >> slot) & 1)) break;
+            clean_phase ^= 1u << slot;
+          }
+          const bool pv = u >= 0 && u < nt, qk = w < nt;
+          const int buf = (c + w) & 1;  // of step w and of step u
+          if (pv && !wait(&p_full[t][buf], ((c + u) >> 1) & 1)) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (pv) {
+              const uint64_t b = v_desc + (uint64_t)((slot * Smem::kKv) >> 4);
 #pragma unroll
-          for (int h = 0; h < HD / 64; ++h) {
-            uint4* at = reinterpret_cast<uint4*>(tile + h * (kStep * 128) + r * 128 + (lane & 7) * 16);
-            uint4 x = *at;
-            // a sign bit for every exponent that is all ones
-            const uint32_t bad = (((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) | ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne)) & 0x80008000u;
-            if (r >= end_row) {
-              *at = make_uint4(0, 0, 0, 0);
-            } else if (bad) {
-              uint32_t w[4] = {x.x, x.y, x.z, x.w};
+              for (int k = 0; k < kStep / 16; ++k)
+                mma_ts(to, ts + buf * kStep + k * 8, b + (uint64_t)((k * 2048) >> 4), kIdO, (u | k) != 0);
+              mma_commit(&o_done[t][buf]);
+            }
+            if (qk) {
+              const uint64_t b = k_desc + (uint64_t)((slot * Smem::kKv) >> 4);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t b = (w[k] & kExp) + kOne;
-                w[k] &= (b & 0x8000u ? 0u : 0xffffu) | (b & 0x80000000u ? 0u : 0xffff0000u);
-              }
-              *at = make_uint4(w[0], w[1], w[2], w[3]);
-              found = true;
+              for (int k = 0; k < HD / 16; ++k)
+                mma_ss(ts + buf * kStep, q_desc + (uint64_t)(((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4),
+                       b + (uint64_t)(((k / 4) * (kStep * 128) + (k % 4) * 32) >> 4), kIdS, k != 0);
+              mma_commit(&s_full[t][buf]);
+            }
+            // the slot (after the last scores the queries too) is free once these products are done; at once
+            // where this tile attends neither
+            if (pv || qk)
+              mma_commit(&empty[slot]);
+            else
+              mbar_arrive(&empty[slot]);
+            if (w == n - 1) {
+              if (qk)
+                mma_commit(&q_empty);
+              else
+                mbar_arrive(&q_empty);
             }
           }
+          __syncwarp();
+          issued = true;
         }
-        if (found) *(volatile int*)&job.dirty = 1;
-        fence_proxy_async_smem();
-        mbar_arrive(&clean[slot]);
+        at += n + 2;
+        c += nt;
       }
-      return true;
-    };
-    int item = blockIdx.x;
-    auto take = [&]() {  // the next job, or one with lane = -1
-      Job job = {};
-      job.lane = -1;
-      while (item < items) {
-        const int over = max(0, item - whole), piece = over % cut, bs = min(item, whole) + over / cut;
-        const int most = item < whole ? 1 : cut, sub = bs % subs, blk = bs / subs;
-        int more = 0;
-        if (lane == 0) more = gridDim.x + atomicAdd(p.queue, 1);
-        item = __shfl_sync(0xffffffffu, more, 0);
-        int b, after;  // the block's lane, the blocks up to its last
-        for (;; scan_base += 32) {
-          int incl = blocks_of(scan_base + lane, false);
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-          }
-          const unsigned has = __ballot_sync(0xffffffffu, blk < scan_done + incl);
-          if (has) {
-            b = scan_base + __ffs(has) - 1;
-            after = scan_done + __shfl_sync(0xffffffffu, incl, __ffs(has) - 1);
-            break;
-          }
-          scan_done += __shfl_sync(0xffffffffu, incl, 31);
-        }
-        job.q0 = p.cu_q[b];
-        job.n_q = p.cu_q[b + 1] - job.q0;
-        job.kv = p.kv_len[b];
-        job.seq = p.seqs ? p.seqs[b] : b;
-        bool ok = job.seq >= 0 && job.seq < s.max_seqs && job.kv >= 0 && job.kv <= s.max_len();
-        if (ok) {
-          // every position of the lane has to have a page of the pool
-          const int32_t* row = p.table + (size_t)job.seq * s.max_pages;
-          const int held = (job.kv + s.page - 1) / s.page;
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ loads of Q and K
+      // Cleans the next V steps of a job that need it, up to step `end`; `first` is the job's first slot.  (This
+      // warp waited for the slots to be free, so it knows which phase of their loads it waits for.)
+      constexpr uint32_t kExp = BF16 ? 0x7f807f80u : 0x7c007c00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
+      int dirty_next = 0;
+      auto clean_steps = [&](Job& job, int first, int end) {
+        const int every = job.kv - job.n_q + job.tok0;  // the last position that every row attends
+        for (; dirty_next < end; ++dirty_next) {
+          const int i = first + dirty_next + 2, slot = i % kSlots;
+          if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], (i / kSlots) & 1, abort_p, kPWait))) return false;
+          uint8_t* tile = vs + slot * Smem::kKv;
+          const int pos = (job.u0 + dirty_next) * kStep, end_row = job.kv - pos;  // the first row to zero
+          bool found = false;
 #pragma unroll 4
-          for (int j = lane; j < held; j += 32) {
-            const int pg = row[j];
-            ok = ok && pg >= 0 && pg < s.n_pages;
-          }
-        }
-        if (!__all_sync(0xffffffffu, ok)) {
-          if (lane == 0) atomicOr(p.status, kStatusRange);
-          continue;
-        }
-        job.tok0 = (after - 1 - blk) * 2 * tq;  // a lane's last block first
-        job.head0 = sub * p.pack;
-        job.kvh = job.head0 / p.group;
-        const int shift = job.kv - job.n_q;
-        int n_t[2];
+          for (int r = max(0, every + 1 - pos) + (lane >> 3); r < kStep; r += 4) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          // steps a tile needs, by its last token's position
-          const int first = job.tok0 + t * tq, last = shift + min(job.n_q, first + tq) - 1;
-          n_t[t] = first < job.n_q && last >= 0 ? last / kStep + 1 : 0;
+            for (int h = 0; h < HD / 64; ++h) {
+              uint4* at = reinterpret_cast<uint4*>(tile + h * (kStep * 128) + r * 128 + (lane & 7) * 16);
+              uint4 x = *at;
+              // a sign bit for every exponent that is all ones
+              const uint32_t bad = (((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) | ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne)) & 0x80008000u;
+              if (r >= end_row) {
+                *at = make_uint4(0, 0, 0, 0);
+              } else if (bad) {
+                uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t b = (w[k] & kExp) + kOne;
+                  w[k] &= (b & 0x8000u ? 0u : 0xffffu) | (b & 0x80000000u ? 0u : 0xffff0000u);
+                }
+                *at = make_uint4(w[0], w[1], w[2], w[3]);
+                found = true;
+              }
+            }
+          }
+          if (found) *(volatile int*)&job.dirty = 1;
+          fence_proxy_async_smem();
+          mbar_arrive(&clean[slot]);
         }
-        const int all = max(n_t[0], n_t[1]);
-        job.pieces = max(1, min(most, all / kPieceSteps));
-        if (piece >= job.pieces) continue;
-        const int each = (all + job.pieces - 1) / job.pieces;
-        job.piece = piece;
-        job.slot = (bs - whole) * cut;
-        job.u0 = piece * each;
-        job.n = max(0, min(each, all - job.u0));
-        for (int t = 0; t < 2; ++t) job.n_t[t] = max(0, min(job.n, n_t[t] - job.u0));
-        job.dirty_from = max(0, max(0, shift + job.tok0 + 1) / kStep - job.u0);
-        job.lane = b;
-        break;
-      }
-      return job;
-    };
-    bool good = true;
-    Job next = take();
-    for (int nj = 0; good;) {
-      const Job job = next;
-      if (nj > 0) {  // what the job before has left, its last four slots
-        Job& last = jobs[(nj - 1) & 1];
-        good = clean_steps(last, loads - last.n - 2, last.n);
-      }
-      if (good && nj >= 2) good = __all_sync(0xffffffffu, mbar_wait(&job_empty[nj & 1], ((nj >> 1) - 1) & 1, abort_p, kPWait));
-      if (!good) break;
-      if (lane == 0) {
-        jobs[nj & 1] = job;
-        mbar_arrive(&job_full[nj & 1]);
-      }
-      __syncwarp();
-      if (job.lane < 0) break;
-      const int n = job.n;
-      if (n == 0) {
-        next = take();
-        // q_full's and q_empty's phases go by jobs: an empty one passes its turn on
+        return true;
+      };
+      bool good = true;
+      for (int nj = 0; good; ++nj) {
+        if (!(good = __all_sync(0xffffffffu, mbar_wait(&job_full[nj & 1], (nj >> 1) & 1, abort_p, kPWait)))) break;
+        const Job job = jobs[nj & 1];
+        if (job.lane < 0) break;
+        const int n = job.n;
         if (nj > 0 && !(good = __all_sync(0xffffffffu, mbar_wait(&q_empty, (nj - 1) & 1, abort_p, kPWait)))) break;
-        if (lane == 0) {
-          mbar_arrive(&q_full);
-          mbar_arrive(&q_empty);
-          mbar_arrive(&q_empty);
+        if (n == 0) {
+          // q_full's and q_empty's phases go by jobs: an empty one passes its turn on
+          if (lane == 0) {
+            mbar_arrive(&want);
+            mbar_arrive(&q_full);
+            mbar_arrive(&q_empty);
+            mbar_arrive(&q_empty);
+          }
+        } else {
+          if (lane == 0) {
+            mbar_expect_tx(&q_full, 2 * Smem::kQ);
+            for (int t = 0; t < 2; ++t)
+              for (int h = 0; h < HD / 64; ++h)
+                tma_load_3d(qs + t * Smem::kQ + h * (kTile * 128), &tmQ, h * 64, job.head0, job.q0 + job.tok0 + t * tq, &q_full);
+          }
+          q_loads = nj + 1;
+          // the load of turn w waits for turn w - 4, which waits for its V step, w - 6, to be clean
+          dirty_next = job.dirty_from;
+          const int first = loads;
+          good = load_steps(job, &tmK, ks, 0, [&](int w) {
+            if (w == max(0, n - kAhead) && lane == 0) mbar_arrive(&want);
+            return clean_steps(jobs[nj & 1], first, w - 5);
+          });
+          if (good) good = clean_steps(jobs[nj & 1], first, n);
         }
-        ++nj;
-        continue;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&job_empty[nj & 1]);
       }
-      if (nj > 0 && !(good = __all_sync(0xffffffffu, mbar_wait(&q_empty, (nj - 1) & 1, abort_p, kPWait)))) break;
-      if (lane == 0) {
-        mbar_expect_tx(&q_full, 2 * Smem::kQ);
-        for (int t = 0; t < 2; ++t)
-          for (int h = 0; h < HD / 64; ++h)
-            tma_load_3d(qs + t * Smem::kQ + h * (kTile * 128), &tmQ, h * 64, job.head0, job.q0 + job.tok0 + t * tq, &q_full);
+    } else if (warp == 10) {
+      // ------------------------------------------------------------ loads of V
+      bool good = true;
+      for (int nj = 0; good; ++nj) {
+        if (!(good = __all_sync(0xffffffffu, mbar_wait(&job_full[nj & 1], (nj >> 1) & 1, abort_p, kPWait)))) break;
+        const Job job = jobs[nj & 1];
+        if (job.lane < 0) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&job_empty[nj & 1]);
+        if (job.n > 0) good = load_steps(job, &tmV, vs, 2, [](int) { return true; });
       }
-      q_loads = ++nj;
-      // the load of turn w waits for turn w - 4, which waits for its V step, w - 6, to be clean
-      dirty_next = job.dirty_from;
-      const int first = loads;
-      good = load_steps(job, &tmK, ks, 0, [&](int w) {
-        // while the ring is full, but late: what is taken early is missing where a CTA runs out of work
-        if (w == max(min(kSlots, n + 1), n - kSlots)) next = take();
-        return clean_steps(jobs[(nj - 1) & 1], first, w - 5);
-      });
-    }
-  } else if (warp == 10) {
-    // ------------------------------------------------------------ loads of V
-    bool good = true;
-    for (int nj = 0; good; ++nj) {
-      if (!(good = __all_sync(0xffffffffu, mbar_wait(&job_full[nj & 1], (nj >> 1) & 1, abort_p, kPWait)))) break;
-      const Job job = jobs[nj & 1];
-      if (job.lane < 0) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&job_empty[nj & 1]);
-      if (job.n > 0) good = load_steps(job, &tmV, vs, 2, [](int) { return true; });
+    } else if (warp == 12) {
+      // ------------------------------------------------------------ work
+      // the blocks of 2 x tq tokens of 32 lanes at a time; a lane whose rows are out of range has none
+      auto blocks_of = [&](int b, bool note) {
+        if (b >= p.n_lanes) return 0;
+        const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
+        if (q0 >= 0 && q1 <= p.n_rows && q1 >= q0) return (q1 - q0 + 2 * tq - 1) / (2 * tq);
+        if (note) atomicOr(p.status, kStatusRange);
+        return 0;
+      };
+      int blocks = 0, longest = 0;
+      for (int base = 0; base < p.n_lanes; base += 32) {
+        blocks += __reduce_add_sync(0xffffffffu, blocks_of(base + lane, blockIdx.x == 0));
+        if (base + lane < p.n_lanes) longest = max(longest, p.kv_len[base + lane]);
+      }
+      longest = __reduce_max_sync(0xffffffffu, longest);
+      int scan_base = 0, scan_done = 0;  // items only grow: the scan for a lane goes on where the last one stopped
+      // Blocks beyond the last full round over the CTAs are cut into `cut` pieces (a short one into fewer), so that
+      // they take less than a round of their own: the least of rounds x (piece + what a piece costs besides).  Not
+      // where most blocks are too short for it: every piece that there is not is work taken in vain.
+      const int sms = gridDim.x, whole = blocks * subs / sms * sms, rest = blocks * subs - whole;
+      int cut = 1;
+      float best = 1.0f;
+      for (int r = 1; r < 4 && rest > 0; ++r) {
+        const int c = min(min(p.pieces, longest / (2 * kPieceSteps * kStep)), min(r * sms, kPromptPieces) / rest);
+        const float cost = (float)((rest * c + sms - 1) / sms) * (1.0f / (float)c + 0.05f);
+        if (c > 1 && cost < best) {
+          cut = c;
+          best = cost;
+        }
+      }
+      const int items = whole + rest * cut;
+      int item = blockIdx.x;
+      auto take = [&]() {  // the next job, or one with lane = -1
+        Job job = {};
+        job.lane = -1;
+        while (item < items) {
+          const int over = max(0, item - whole), piece = over % cut, bs = min(item, whole) + over / cut;
+          const int most = item < whole ? 1 : cut, sub = bs % subs, blk = bs / subs;
+          int more = 0;
+          if (lane == 0) more = gridDim.x + atomicAdd(p.queue, 1);
+          item = __shfl_sync(0xffffffffu, more, 0);
+          int b, after;  // the block's lane, the blocks up to its last
+          for (;; scan_base += 32) {
+            int incl = blocks_of(scan_base + lane, false);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const int y = __shfl_up_sync(0xffffffffu, incl, o);
+              if (lane >= o) incl += y;
+            }
+            const unsigned has = __ballot_sync(0xffffffffu, blk < scan_done + incl);
+            if (has) {
+              b = scan_base + __ffs(has) - 1;
+              after = scan_done + __shfl_sync(0xffffffffu, incl, __ffs(has) - 1);
+              break;
+            }
+            scan_done += __shfl_sync(0xffffffffu, incl, 31);
+          }
+          job.q0 = p.cu_q[b];
+          job.n_q = p.cu_q[b + 1] - job.q0;
+          job.kv = p.kv_len[b];
+          job.seq = p.seqs ? p.seqs[b] : b;
+          bool ok = job.seq >= 0 && job.seq < s.max_seqs && job.kv >= 0 && job.kv <= s.max_len();
+          if (ok) {
+            // every position of the lane has to have a page of the pool
+            const int32_t* row = p.table + (size_t)job.seq * s.max_pages;
+            const int held = (job.kv + s.page - 1) / s.page;
+#pragma unroll 4
+            for (int j = lane; j < held; j += 32) {
+              const int pg = row[j];
+              ok = ok && pg >= 0 && pg < s.n_pages;
+            }
+          }
+          if (!__all_sync(0xffffffffu, ok)) {
+            if (lane == 0) atomicOr(p.status, kStatusRange);
+            continue;
+          }
+          job.tok0 = (after - 1 - blk) * 2 * tq;  // a lane's last block first
+          job.head0 = sub * p.pack;
+          job.kvh = job.head0 / p.group;
+          const int shift = job.kv - job.n_q;
+          int n_t[2];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            // steps a tile needs, by its last token's position
+            const int first = job.tok0 + t * tq, last = shift + min(job.n_q, first + tq) - 1;
+            n_t[t] = first < job.n_q && last >= 0 ? last / kStep + 1 : 0;
+          }
+          const int all = max(n_t[0], n_t[1]);
+          job.pieces = max(1, min(most, all / kPieceSteps));
+          if (piece >= job.pieces) continue;
+          const int each = (all + job.pieces - 1) / job.pieces;
+          job.piece = piece;
+          job.slot = (bs - whole) * cut;
+          job.u0 = piece * each;
+          job.n = max(0, min(each, all - job.u0));
+          for (int t = 0; t < 2; ++t) job.n_t[t] = max(0, min(job.n, n_t[t] - job.u0));
+          job.dirty_from = max(0, max(0, shift + job.tok0 + 1) / kStep - job.u0);
+          job.lane = b;
+          break;
+        }
+        return job;
+      };
+      bool good = true;
+      for (int nj = 0; good; ++nj) {
+        // late, when the job before nears its end: what is taken early is missing where a CTA runs out of work
+        if (nj > 0 && !(good = __all_sync(0xffffffffu, mbar_wait(&want, (nj - 1) & 1, abort_p, kPWait)))) break;
+        const Job job = take();
+        if (nj >= 2 && !(good = __all_sync(0xffffffffu, mbar_wait(&job_empty[nj & 1], ((nj >> 1) - 1) & 1, abort_p, kPWait)))) break;
+        if (lane == 0) {
+          jobs[nj & 1] = job;
+          mbar_arrive(&job_full[nj & 1]);
+        }
+        __syncwarp();
+        if (job.lane < 0) break;
+      }
     }
   }
 
