@@ -56,6 +56,7 @@ constexpr int kPromptThreads = 512;
 constexpr int kTile = 128;                // query rows of a tile
 constexpr int kStep = 64;                 // positions of a step
 constexpr int kSms = 148;
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // of 128 at launch
 constexpr int kAhead = 8;                 // turns before a job's last that the next one is taken
 constexpr long long kPWait = 4000000000ll;  // SM clocks
 constexpr float kLog2e = 1.4426950408889634f;
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 
   // Registers: 512 x 128 at launch = 256 x 184 (softmax: a thread holds a row of S) + 256 x 72.
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ------------------------------------------------------------ softmax of tile t, row r
     const int t = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the outputs are written
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 8 || warp == 11) {
       // ------------------------------------------------------------ products of tile t
       const int t = warp == 11;
@@ -875,17 +876,23 @@ bool make_tmap3(CUtensorMap* tm, const void* base, bool bf16, uint64_t x, uint64
   const cuuint32_t box[3] = {box_x, box_y, box_z}, estr[3] = {1, 1, 1};
   return enc(tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base),
              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             box_x == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             box_x == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int HD, bool BF16>
 cudaError_t launch_as(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, const CUtensorMap& tmO,
-                      const PromptParams& p,
-                      long long blocks, cudaStream_t st) {
+                      const PromptParams& p, long long blocks, cudaStream_t st) {
   int limit = 0;
   cudaError_t e = dyn_smem_limit((const void*)paged_prompt_kernel<HD, BF16>, &limit);
   if (e != cudaSuccess) return e;
   if (PromptSmem<HD>::kBytes > limit) return cudaErrorInvalidConfiguration;
+  // the kernel's split of registers between its roles needs what it was written for at launch
+  static const int regs = [] {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, (const void*)paged_prompt_kernel<HD, BF16>) == cudaSuccess ? fa.numRegs : 0;
+  }();
+  if (regs * kPromptThreads < 256 * (kSoftmaxRegs + kOtherRegs)) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
