@@ -22,8 +22,8 @@
 //             is there while a tile's softmax runs and the tensor pipe has products meanwhile
 //   9, 10     load by TMA, page by page (a page of one K/V head is one box per 64 values): Q and K / V.  A slot of the ring holds what one issue of products takes, K(u+2) and V(u).
 //             (Two warps: a box costs some 50 clocks of issue, a step of 16-position pages 16 boxes.)
-//             Warp 9 also cleans the V steps that hold positions not every row attends: rows past the
-//             cache's end are zeroed (their memory may hold anything) and values that are not finite are
+//             Warp 9 also cleans, with 13 to 15, the V steps that hold positions not every row attends: rows
+//             past the cache's end are zeroed (their memory may hold anything) and values that are not finite are
 //             taken out (0 x inf would reach the rows that do not attend them) and given back at the end
 //             to the rows that do
 //   12        takes work (a job: a block or a piece of one) and looks its lane's pages over, 3 us ahead
@@ -162,6 +162,44 @@ struct Job {
   int slot, piece, pieces;  // where partial results go: (block, heads) and piece
   int dirty;    // a value that is not finite was taken out of V
 };
+
+// A V step to clean: its slot (-1: no more), the first row that not every query row attends, the first row past
+// the cache's end, and where to note that a value was taken out.
+struct Dirty {
+  int slot, row, end;
+  int* noted;
+};
+// Share `part` of four of it, by one warp: 4 rows in 16.
+template <int HD, bool BF16>
+__device__ __forceinline__ void clean_step(uint8_t* tile, const Dirty& d, int part) {
+  constexpr uint32_t kExp = BF16 ? 0x7f807f80u : 0x7c007c00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
+  const int lane = threadIdx.x & 31;
+  bool found = false;
+#pragma unroll 4
+  for (int r = d.row + part * 4 + (lane >> 3); r < kStep; r += 16) {
+#pragma unroll
+    for (int h = 0; h < HD / 64; ++h) {
+      uint4* at = reinterpret_cast<uint4*>(tile + h * (kStep * 128) + r * 128 + (lane & 7) * 16);
+      uint4 x = *at;
+      // a sign bit for every exponent that is all ones
+      const uint32_t bad = (((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) | ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne)) & 0x80008000u;
+      if (r >= d.end) {
+        *at = make_uint4(0, 0, 0, 0);
+      } else if (bad) {
+        uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t b = (w[k] & kExp) + kOne;
+          w[k] &= (b & 0x8000u ? 0u : 0xffffu) | (b & 0x80000000u ? 0u : 0xffff0000u);
+        }
+        *at = make_uint4(w[0], w[1], w[2], w[3]);
+        found = true;
+      }
+    }
+  }
+  if (found) *(volatile int*)d.noted = 1;
+  fence_proxy_async_smem();
+}
 
 // What the warps of a tile agree on when its block is cut into pieces.
 struct Joint {
@@ -354,7 +392,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   __shared__ uint64_t q_full, q_empty, full[kSlots], empty[kSlots], clean[kSlots];
   __shared__ uint64_t s_full[2][2], p_full[2][2], o_done[2][2], job_full[2], job_empty[2], fin[2];
   __shared__ uint32_t tmem_base;
-  __shared__ uint64_t want;
+  __shared__ uint64_t want, go;
+  __shared__ Dirty dirt;
   __shared__ int abort_flag;
   __shared__ Joint joint_mem;
   Joint* joint = &joint_mem;
@@ -369,11 +408,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(&q_full, 1);
     mbar_init(&want, 1);
+    mbar_init(&go, 1);
     mbar_init(&q_empty, 2);
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&full[i], 2);   // K's and V's loads
       mbar_init(&empty[i], 2);  // both tiles
-      mbar_init(&clean[i], 32);
+      mbar_init(&clean[i], 128);  // four warps
     }
     for (int t = 0; t < 2; ++t) {
       for (int i = 0; i < 2; ++i) {
@@ -614,42 +654,31 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     } else if (warp == 9) {
       // ------------------------------------------------------------ loads of Q and K
-      // Cleans the next V steps of a job that need it, up to step `end`; `first` is the job's first slot.  (This
-      // warp waited for the slots to be free, so it knows which phase of their loads it waits for.)
-      constexpr uint32_t kExp = BF16 ? 0x7f807f80u : 0x7c007c00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
-      int dirty_next = 0;
+      // Has the next V steps of a job cleaned that need it, up to step `end`; `first` is the job's first slot.  (This
+      // warp waited for the slots to be free, so it knows which phase of their loads it waits for.)  Four warps
+      // share a step; the one before is done when the next is given out.
+      int dirty_next = 0, last = -1;  // the slot given out last
+      uint32_t clean_phase = 0;       // one bit per slot
+      auto give_out = [&](const Dirty& d) {
+        if (last >= 0) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&clean[last], (clean_phase >> last) & 1, abort_p, kPWait))) return false;
+          clean_phase ^= 1u << last;
+        }
+        last = d.slot;
+        if (lane == 0) {
+          dirt = d;
+          mbar_arrive(&go);
+        }
+        return true;
+      };
       auto clean_steps = [&](Job& job, int first, int end) {
-        const int every = job.kv - job.n_q + job.tok0;  // the last position that every row attends
         for (; dirty_next < end; ++dirty_next) {
-          const int i = first + dirty_next + 2, slot = i % kSlots;
+          const int i = first + dirty_next + 2, slot = i % kSlots, pos = (job.u0 + dirty_next) * kStep;
           if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], (i / kSlots) & 1, abort_p, kPWait))) return false;
-          uint8_t* tile = vs + slot * Smem::kKv;
-          const int pos = (job.u0 + dirty_next) * kStep, end_row = job.kv - pos;  // the first row to zero
-          bool found = false;
-#pragma unroll 4
-          for (int r = max(0, every + 1 - pos) + (lane >> 3); r < kStep; r += 4) {
-#pragma unroll
-            for (int h = 0; h < HD / 64; ++h) {
-              uint4* at = reinterpret_cast<uint4*>(tile + h * (kStep * 128) + r * 128 + (lane & 7) * 16);
-              uint4 x = *at;
-              // a sign bit for every exponent that is all ones
-              const uint32_t bad = (((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) | ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne)) & 0x80008000u;
-              if (r >= end_row) {
-                *at = make_uint4(0, 0, 0, 0);
-              } else if (bad) {
-                uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const uint32_t b = (w[k] & kExp) + kOne;
-                  w[k] &= (b & 0x8000u ? 0u : 0xffffu) | (b & 0x80000000u ? 0u : 0xffff0000u);
-                }
-                *at = make_uint4(w[0], w[1], w[2], w[3]);
-                found = true;
-              }
-            }
-          }
-          if (found) *(volatile int*)&job.dirty = 1;
-          fence_proxy_async_smem();
+          // not attended by every row: the positions behind the first query's
+          const Dirty d{slot, max(0, job.kv - job.n_q + job.tok0 + 1 - pos), job.kv - pos, &job.dirty};
+          if (!give_out(d)) return false;
+          clean_step<HD, BF16>(vs + slot * Smem::kKv, d, 0);
           mbar_arrive(&clean[slot]);
         }
         return true;
@@ -689,6 +718,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&job_empty[nj & 1]);
       }
+      if (good) give_out(Dirty{-1, 0, 0, nullptr});  // no more
     } else if (warp == 10) {
       // ------------------------------------------------------------ loads of V
       bool good = true;
@@ -815,6 +845,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         __syncwarp();
         if (job.lane < 0) break;
+      }
+    } else if (warp > 12) {
+      // ------------------------------------------------------------ cleaning, with warp 9
+      for (int g = 0; mbar_wait(&go, g & 1, abort_p, kPWait); ++g) {
+        const Dirty d = dirt;
+        if (d.slot < 0) break;
+        clean_step<HD, BF16>(vs + d.slot * Smem::kKv, d, warp - 12);
+        mbar_arrive(&clean[d.slot]);
       }
     }
   }
