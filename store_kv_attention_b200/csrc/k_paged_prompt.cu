@@ -763,15 +763,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
       const int items = whole + rest * cut;
       int item = blockIdx.x;
+      bool own = true;  // a CTA's first item is its own
       auto take = [&]() {  // the next job, or one with lane = -1
         Job job = {};
         job.lane = -1;
-        while (item < items) {
+        for (;;) {
+          if (!own) {
+            int more = 0;
+            if (lane == 0) more = gridDim.x + atomicAdd(p.queue, 1);
+            item = __shfl_sync(0xffffffffu, more, 0);
+          }
+          own = false;
+          if (item >= items) break;
           const int over = max(0, item - whole), piece = over % cut, bs = min(item, whole) + over / cut;
           const int most = item < whole ? 1 : cut, sub = bs % subs, blk = bs / subs;
-          int more = 0;
-          if (lane == 0) more = gridDim.x + atomicAdd(p.queue, 1);
-          item = __shfl_sync(0xffffffffu, more, 0);
           int b, after;  // the block's lane, the blocks up to its last
           for (;; scan_base += 32) {
             int incl = blocks_of(scan_base + lane, false);
