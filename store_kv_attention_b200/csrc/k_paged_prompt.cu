@@ -777,8 +777,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (item >= items) break;
           const int over = max(0, item - whole), piece = over % cut, bs = min(item, whole) + over / cut;
           const int most = item < whole ? 1 : cut, sub = bs % subs, blk = bs / subs;
-          int b, after;  // the block's lane, the blocks up to its last
-          for (;; scan_base += 32) {
+          int b = -1, after = 0;  // the block's lane, the blocks up to its last
+          for (; scan_base < p.n_lanes; scan_base += 32) {
             int incl = blocks_of(scan_base + lane, false);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -793,6 +793,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
             scan_done += __shfl_sync(0xffffffffu, incl, 31);
           }
+          if (b < 0) break;  // only where cu_q decreases and the blocks' count has overflowed
           job.q0 = p.cu_q[b];
           job.n_q = p.cu_q[b + 1] - job.q0;
           job.kv = p.kv_len[b];
