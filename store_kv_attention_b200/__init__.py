@@ -551,10 +551,7 @@ class PagedCache:
         return PagedCacheC(*(t.data_ptr() for t in self._buffers))
 
 
-def _paged_tensor(cache: PagedCache, name: str, t, dtype, shape) -> None:
-    """Raises unless t is dense, on the cache's device, with this type and shape."""
-    if t.dtype is dtype and t.get_device() == cache._index and t.shape == shape and t.is_contiguous():
-        return
+def _paged_refuse(cache: PagedCache, name: str, t, dtype, shape) -> None:
     if t.device != cache.device:
         raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
     if t.dtype != dtype:
@@ -564,21 +561,30 @@ def _paged_tensor(cache: PagedCache, name: str, t, dtype, shape) -> None:
     raise ValueError(f"{name} is not dense: strides {t.stride()}")
 
 
+def _paged_tensor(cache: PagedCache, name: str, t, dtype, shape) -> None:
+    """Raises unless t is dense, on the cache's device, with this type and shape."""
+    if not (t.dtype is dtype and t.get_device() == cache._index and t.shape == shape and t.is_contiguous()):
+        _paged_refuse(cache, name, t, dtype, shape)
+
+
 def _paged_rows(cache: PagedCache, name: str, t, n: int, heads: int) -> int:
     """The row stride of t [n, heads, head_dim], whose rows may be parts of wider ones (0: dense)."""
-    shape = (n, heads, cache.desc.head_dim)
-    if t.shape == shape and not t.is_contiguous() and t.stride(2) == 1 and t.stride(1) == shape[2] and t.stride(0) > 0:
-        _paged_tensor(cache, name, t[0], cache.dtype, shape[1:])
-        return t.stride(0)
-    _paged_tensor(cache, name, t, cache.dtype, shape)
-    return 0
+    hd = cache.desc.head_dim
+    if t.dtype is cache.dtype and t.get_device() == cache._index and t.shape == (n, heads, hd):
+        if t.is_contiguous():
+            return 0
+        rows, head, one = t.stride()
+        if rows > 0 and one == 1 and (head == hd or heads == 1):
+            return rows
+    _paged_refuse(cache, name, t, cache.dtype, (n, heads, hd))
 
 
 def _paged_ints(cache: PagedCache, name: str, t, n: int) -> Optional[int]:
     """The address of t, int32 [n] on the cache's device (None -> NULL)."""
     if t is None:
         return None
-    _paged_tensor(cache, name, t, cache._int32, (n,))
+    if not (t.dtype is cache._int32 and t.get_device() == cache._index and t.shape == (n,) and t.is_contiguous()):
+        _paged_refuse(cache, name, t, cache._int32, (n,))
     return t.data_ptr()
 
 
