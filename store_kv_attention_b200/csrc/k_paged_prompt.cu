@@ -124,6 +124,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -241,26 +246,35 @@ __device__ __forceinline__ bool finish_rows(const PromptParams& p, const CUtenso
   const int row0 = (warp & 3) * 32;
   const bool all = first + ((row0 + 31) >> log_pack) < job.n_q;
   const int to_head = job.head0 + (row0 & ((1 << log_pack) - 1)), to_row = job.q0 + first + (row0 >> log_pack);
-  auto put = [&](int d, const float* y) {
+  auto stage_words = [&](int d, const uint32_t* w) {
     const uint32_t buf = stage + (d / 32 & 1) * 2048;
     if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the store before the last has read this buffer
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)),
-                   "r"(pack16<BF16>(y[8 * i], y[8 * i + 1])), "r"(pack16<BF16>(y[8 * i + 2], y[8 * i + 3])),
-                   "r"(pack16<BF16>(y[8 * i + 4], y[8 * i + 5])), "r"(pack16<BF16>(y[8 * i + 6], y[8 * i + 7]))
+                   "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
                    : "memory");
+    return buf;
+  };
+  auto store_rows = [&](int d, uint32_t buf) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                       reinterpret_cast<uint64_t>(tmO)),
+                   "r"(d), "r"(to_head), "r"(to_row), "r"(buf)
+                   : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+  };
+  auto put = [&](int d, const float* y) {
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack16<BF16>(y[2 * i], y[2 * i + 1]);
+    const uint32_t buf = stage_words(d, w);
     if (all) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                         reinterpret_cast<uint64_t>(tmO)),
-                     "r"(d), "r"(to_head), "r"(to_row), "r"(buf)
-                     : "memory");
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-      }
+      store_rows(d, buf);
       return;
     }
     __syncwarp();
@@ -279,6 +293,25 @@ __device__ __forceinline__ bool finish_rows(const PromptParams& p, const CUtenso
   };
   if (first >= job.n_q) {
     // a tile without tokens
+  } else if (job.pieces == 1 && all && nt > 0 && !__any_sync(0xffffffffu, fix)) {
+    // the usual case.  (Unrolled, the kernel's larger code cost more than it saved: packed prompts 214 us a call
+    // against 192, 16384 tokens 962 against 925.)
+    const float inv = 1.0f / l;
+    const uint64_t inv2 = pair(inv, inv);
+#pragma unroll 1
+    for (int d = 0; d < HD; d += 32) {
+      uint32_t o[32], w[16];
+      tmem_ld32(to + d, o);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(o[i]));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 y = unpair(mul2(pair(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), inv2));
+        w[i] = attends ? pack16<BF16>(y.x, y.y) : 0u;
+      }
+      store_rows(d, stage_words(d, w));
+    }
   } else if (job.pieces == 1) {
     const float inv = 1.0f / l;
 #pragma unroll 1
