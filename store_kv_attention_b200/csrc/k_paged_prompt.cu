@@ -31,11 +31,14 @@
 // time: the base of the exponents is a free choice (P then reaches 2^8 and its sum 2^8 times the
 // positions, far inside FP32), and the rescale, a round trip of O through registers, becomes rare.
 //
-// Measured: 16384 tokens, 16 heads over 4 K/V heads x 128, 929 us in long loops (1.18 PFLOP/s, power bound at
-// 1.47 GHz), 788 us in short ones: about 1440 clocks a step, the two tiles' products being 1024 at the tensor pipe's
-// rate, or 1280 with the scores' operands (6 KB a product of 128 x 64 x 16) at 128 bytes a clock from shared
-// memory; the exponentials 1024.  Steps of 128 with one S buffer a tile took 1720 (softmax, then products, one behind
-// the other).  A job costs about 9000 clocks besides its steps.
+// Measured: 16384 tokens, 16 heads over 4 K/V heads x 128, 915 to 940 us in long loops (1.17 to 1.20 PFLOP/s, power
+// bound: the clock falls to 1.40 GHz), 820 us in short ones at 1.59 GHz: about 1380 clocks a step, the two tiles'
+// products being 1024 at the tensor pipe's rate, or 1280 with the scores' operands (6 KB a product of 128 x 64 x 16)
+// at 128 bytes a clock from shared memory; the exponentials 1024.  Steps of 128 with one S buffer a tile took 1720
+// (softmax, then products, one behind the other); the exponentials of the two tiles taking turns on a scheduler,
+// 1600.  A job costs about 6000 clocks besides its steps: 1100 until its last product is done, 2400 for O / sum and its
+// stores, 1200 for the next one's first softmax; a CTA's first job starts 11 000 clocks after the launch, by the chain
+// of loads of the work, the pages, Q and K and by code that is fetched for the first time.
 //
 // TMEM (512 columns): S_0 (two buffers) | S_1 (128 columns each; P over a buffer's first 32) | O_0 | O_1.
 #include <cuda.h>
