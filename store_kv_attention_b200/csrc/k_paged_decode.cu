@@ -373,23 +373,17 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Deco
   }
 }
 
-// Joins the splits of one (lane, query head): a thread four values of every kAtOnce-th split, eight loads in
-// flight.  (The last CTA of a lane joining its splits inside the kernel above was measured instead: the fence
-// and the counter's round trip stand at the end of every split, 10.1 us a call against 8.9 at one lane of
+// Joins the n splits of one (lane, query head), COLS of its values: a thread four values of every kAtOnce-th split,
+// eight loads in flight.  (The last CTA of a lane joining its splits inside the kernel above was measured instead: the
+// fence and the counter's round trip stand at the end of every split, 10.1 us a call against 8.9 at one lane of
 // 2049, 193 us against 184 at 32 lanes of 4097.)
 constexpr int kJoinThreads = 256;
-template <int HD, bool BF16>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const DecodeParams p) {
-  constexpr int kLanes = HD / 4, kAtOnce = kJoinThreads / kLanes, kWindow = kAtOnce * 8;  // splits a round
+template <int HD, int COLS, bool BF16>
+__device__ __forceinline__ void join_splits(const DecodeParams& p, int n) {
+  constexpr int kLanes = COLS / 4, kAtOnce = kJoinThreads / kLanes, kWindow = kAtOnce * 8;  // splits a round
   __shared__ float4 part[kAtOnce][kLanes];
   __shared__ float weight[kWindow], psum[kJoinThreads / 32], pmax[kJoinThreads / 32];
-  ptx::pdl_wait();
-  ptx::pdl_trigger();
-  const int h = blockIdx.x, b = blockIdx.y, t = threadIdx.x;
-  int seq;
-  const int len = lane_len(p, b, &seq);
-  const int n = len < 0 ? 0 : paged_splits(len, p.target, p.rows);
-  if (n <= 1) return;  // a single split wrote the output itself
+  const int h = blockIdx.x, b = blockIdx.y, t = threadIdx.x, col = blockIdx.z * COLS;
   const size_t first = ((size_t)b * p.n_heads + h) * p.s_max;
   const float2* ml = reinterpret_cast<const float2*>(p.ml) + first;
   const int d = t % kLanes, g = t / kLanes;
@@ -400,7 +394,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const DecodePa
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int i = i0 + k * kAtOnce + g;
-      if (i < n) x[k] = *reinterpret_cast<const float4*>(p.acc + (first + i) * HD + d * 4);
+      if (i < n) x[k] = *reinterpret_cast<const float4*>(p.acc + (first + i) * HD + col + d * 4);
     }
     const float2 s = t < kWindow && i0 + t < n ? ml[i0 + t] : make_float2(-INFINITY, 0.0f);
     float mx = s.x;
@@ -448,9 +442,27 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const DecodePa
       a.w += y.w;
     }
     const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-    *reinterpret_cast<uint2*>(p.out + ((size_t)b * p.n_heads + h) * HD + d * 4) =
+    *reinterpret_cast<uint2*>(p.out + ((size_t)b * p.n_heads + h) * HD + col + d * 4) =
         make_uint2(pack16<BF16>(a.x * inv, a.y * inv), pack16<BF16>(a.z * inv, a.w * inv));
   }
+}
+
+// More than kJoinWide splits are joined by HD / 32 CTAs, 32 values each, a round of 256 splits then: one lane of 60000
+// over 148 splits 20.6 -> 19.5 us a call, of 40000 over 74 23.3 -> 21.8; with fewer, one CTA takes them in a round as it
+// is (37 splits the same, 48 lanes of up to 8 splits 150 us against 136).  By the lane's own splits, so that its bits
+// depend on nothing else.
+constexpr int kJoinWide = 64;
+template <int HD, bool BF16>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const DecodeParams p) {
+  ptx::pdl_wait();
+  ptx::pdl_trigger();
+  int seq;
+  const int len = lane_len(p, blockIdx.y, &seq), n = len < 0 ? 0 : paged_splits(len, p.target, p.rows);
+  if (n <= 1) return;  // a single split wrote the output itself
+  if (n > kJoinWide)
+    join_splits<HD, 32, BF16>(p, n);
+  else if (blockIdx.z == 0)
+    join_splits<HD, HD, BF16>(p, n);
 }
 
 template <int HD, bool BF16>
@@ -474,7 +486,7 @@ cudaError_t launch_as(const DecodeParams& p, cudaStream_t st) {
   count_launch();
   if (e != cudaSuccess) return e;
   if (p.s_max > 1) {
-    cfg.gridDim = dim3((unsigned)p.n_heads, (unsigned)p.n_lanes);
+    cfg.gridDim = dim3((unsigned)p.n_heads, (unsigned)p.n_lanes, p.s_max > kJoinWide ? HD / 32 : 1);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, paged_join_kernel<HD, BF16>, p);

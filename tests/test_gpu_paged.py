@@ -190,6 +190,25 @@ def test_decode_lanes_do_not_depend_on_each_other(tl):
     assert torch.equal(out, solo)
 
 
+@pytest.mark.parametrize("hd,dtype", [(64, FP16), (128, BF16)])
+def test_decode_joins_many_splits(tl, hd, dtype):
+    """Lanes of 64, 65, 301, 1, no and 2 splits in one call; a lane's bits are those it has in a shorter table."""
+    lens = [64 * 128, 64 * 128 + 1, 300 * 128 + 5, 1, 0, 129]
+    rig = Rig(tl, lens, kv=1, group=2, hd=hd, page=64, dtype=dtype, layers=1, split=128)
+    q = rig.queries(6)
+    out = torch.full_like(q, float("nan"))
+    tl.paged_attn_decode(rig.cache, 0, q, _i32(lens), out)
+    rig.ok()
+    rig.check_decode(0, q, out)
+    c = rig.cache
+    d = tl.PagedDesc(1, c.desc.n_pages, 64, 1, hd, c.desc.max_seqs, 128, c.desc.dtype)
+    short = tl.PagedCache(d, 2, 1, split_rows=128, k=c.k, v=c.v, table=c.table[:, :128].contiguous(), refs=c.refs)
+    solo = torch.empty_like(q[:1])
+    tl.paged_attn_decode(short, 0, q[:1], _i32(lens[:1]), solo)
+    assert tl.poll_status(short) == tl.TL_OK
+    assert torch.equal(out[:1], solo)
+
+
 def test_decode_skips_and_reports(tl):
     """Lanes out of range are not written; positions without a page are left out."""
     lens = [40, 40, 40, 40]
