@@ -242,10 +242,56 @@ struct Joint {
   int last[2];
 };
 
-// The end of a tile's job, by the threads of its rows: O / l into the output, or the piece's part into the
-// workspace and, by the last piece, the parts joined.  False: a wait gave up.
+// 32 values of every row of a warp into shared memory (64-byte rows, 64-byte swizzle), in two buffers by turns.
+__device__ __forceinline__ uint32_t stage_words(uint32_t stage, int d, const uint32_t* w) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t buf = stage + (d / 32 & 1) * 2048;
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the store before the last has read this buffer
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)),
+                 "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
+                 : "memory");
+  return buf;
+}
+// From there into the output: by one TMA store, where all rows are the lane's.
+__device__ __forceinline__ void store_rows(const CUtensorMap* tmO, int d, int head, int row, uint32_t buf) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(tmO)),
+                 "r"(d), "r"(head), "r"(row), "r"(buf)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+
+// Where some are not: four lanes write 64 bytes of a row.
+template <int HD>
+__device__ __forceinline__ void copy_rows(const PromptParams& p, const Job& job, int first, int log_pack, int row0, int d,
+                                          uint32_t buf) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const int wr = i * 8 + (lane >> 2), row = row0 + wr, to_tok = first + (row >> log_pack);
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(buf + wr * 64 + (((lane & 3) ^ ((wr >> 1) & 3)) << 4))
+                 : "memory");
+    if (to_tok < job.n_q)
+      *reinterpret_cast<uint4*>(p.out + ((size_t)(job.q0 + to_tok) * p.n_heads + job.head0 + (row & ((1 << log_pack) - 1))) * HD + d +
+                                (lane & 3) * 8) = v;
+  }
+}
+
+// The end of a tile's job where the usual one does not do: a tile that attends nothing; values to give back; the part of
+// a piece into the workspace and, by the last piece, the parts joined.  False: a wait gave up.
 template <int HD, bool BF16>
-__device__ __forceinline__ bool finish_rows(const PromptParams& p, const CUtensorMap* tmO, const Job& job, int t,
+__device__ __noinline__ bool finish_rare(const PromptParams& p, const CUtensorMap* tmO, const Job& job, int t,
                                          int log_pack, uint32_t to, uint32_t stage, float m, float l, Joint* joint,
                                          int& parts, volatile int* abort) {
   constexpr int kPartFloats = kTile * (HD + 2);
@@ -271,78 +317,21 @@ __device__ __forceinline__ bool finish_rows(const PromptParams& p, const CUtenso
       }
     }
   };
-  // 32 values of every row of the warp through shared memory (64-byte rows, 64-byte swizzle), in two buffers by
-  // turns: one TMA store where all rows are the lane's, else four lanes write 64 bytes of a row
   const int row0 = (warp & 3) * 32;
   const bool all = first + ((row0 + 31) >> log_pack) < job.n_q;
   const int to_head = job.head0 + (row0 & ((1 << log_pack) - 1)), to_row = job.q0 + first + (row0 >> log_pack);
-  auto stage_words = [&](int d, const uint32_t* w) {
-    const uint32_t buf = stage + (d / 32 & 1) * 2048;
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the store before the last has read this buffer
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)),
-                   "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
-                   : "memory");
-    return buf;
-  };
-  auto store_rows = [&](int d, uint32_t buf) {
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                       reinterpret_cast<uint64_t>(tmO)),
-                   "r"(d), "r"(to_head), "r"(to_row), "r"(buf)
-                   : "memory");
-      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    }
-  };
   auto put = [&](int d, const float* y) {
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = pack16<BF16>(y[2 * i], y[2 * i + 1]);
-    const uint32_t buf = stage_words(d, w);
+    const uint32_t buf = stage_words(stage, d, w);
     if (all) {
-      store_rows(d, buf);
+      store_rows(tmO, d, to_head, to_row, buf);
       return;
     }
-    __syncwarp();
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-      const int wr = i * 8 + (lane >> 2), row = row0 + wr, to_tok = first + (row >> log_pack);
-      uint4 v;
-      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                   : "r"(buf + wr * 64 + (((lane & 3) ^ ((wr >> 1) & 3)) << 4))
-                   : "memory");
-      if (to_tok < job.n_q)
-        *reinterpret_cast<uint4*>(p.out + ((size_t)(job.q0 + to_tok) * p.n_heads + job.head0 + (row & ((1 << log_pack) - 1))) * HD + d +
-                                  (lane & 3) * 8) = v;
-    }
+    copy_rows<HD>(p, job, first, log_pack, row0, d, buf);
   };
-  if (first >= job.n_q) {
-    // a tile without tokens
-  } else if (job.pieces == 1 && all && nt > 0 && !__any_sync(0xffffffffu, fix)) {
-    // the usual case.  (Unrolled, the kernel's larger code cost more than it saved: packed prompts 214 us a call
-    // against 192, 16384 tokens 962 against 925.)
-    const float inv = 1.0f / l;
-    const uint64_t inv2 = pair(inv, inv);
-#pragma unroll 1
-    for (int d = 0; d < HD; d += 32) {
-      uint32_t o[32], w[16];
-      tmem_ld32(to + d, o);
-      tmem_ld_wait();
-#pragma unroll
-      for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(o[i]));
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float2 y = unpair(mul2(pair(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), inv2));
-        w[i] = attends ? pack16<BF16>(y.x, y.y) : 0u;
-      }
-      store_rows(d, stage_words(d, w));
-    }
-  } else if (job.pieces == 1) {
+  if (job.pieces == 1) {
     const float inv = 1.0f / l;
 #pragma unroll 1
     for (int d = 0; d < HD; d += 32) {
@@ -437,6 +426,46 @@ __device__ __forceinline__ bool finish_rows(const PromptParams& p, const CUtenso
         put(d, y);
       }
     }
+  }
+  return true;
+}
+
+// The end of a tile's job, by the threads of its rows: O / l into the output.  The cases that are rare or long are a
+// function apart, which the main loop is the faster for (packed prompts 187 -> 184 us a call, chunks 214 -> 211); with
+// this loop unrolled the larger code cost more than it saved (packed prompts 214, 16384 tokens 962 against 925).
+template <int HD, bool BF16>
+__device__ __forceinline__ bool finish_rows(const PromptParams& p, const CUtensorMap* tmO, const Job& job, int t,
+                                            int log_pack, uint32_t to, uint32_t stage, float m, float l, Joint* joint,
+                                            int& parts, volatile int* abort) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x & 127;
+  const int tq = kTile >> log_pack, first = job.tok0 + t * tq, nt = job.n_t[t], row0 = (warp & 3) * 32;
+  const bool all = first + ((row0 + 31) >> log_pack) < job.n_q;
+  if (first >= job.n_q) return true;  // a tile without tokens
+  // one answer for the warp: a step that only the other tile attends may be under cleaning still
+  if (job.pieces > 1 || nt == 0 || __any_sync(0xffffffffu, *(volatile const int*)&job.dirty != 0))
+    return finish_rare<HD, BF16>(p, tmO, job, t, log_pack, to, stage, m, l, joint, parts, abort);
+  const int to_head = job.head0 + (row0 & ((1 << log_pack) - 1)), to_row = job.q0 + first + (row0 >> log_pack);
+  const int lim = min(job.kv - job.n_q + first + (r >> log_pack), job.kv - 1);
+  const bool attends = lim >= 0 && m != -INFINITY;
+  const float inv = 1.0f / l;
+  const uint64_t inv2 = pair(inv, inv);
+#pragma unroll 1
+  for (int d = 0; d < HD; d += 32) {
+    uint32_t o[32], w[16];
+    tmem_ld32(to + d, o);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(o[i]));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 y = unpair(mul2(pair(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), inv2));
+      w[i] = attends ? pack16<BF16>(y.x, y.y) : 0u;
+    }
+    const uint32_t buf = stage_words(stage, d, w);
+    if (all)
+      store_rows(tmO, d, to_head, to_row, buf);
+    else
+      copy_rows<HD>(p, job, first, log_pack, row0, d, buf);
   }
   return true;
 }
