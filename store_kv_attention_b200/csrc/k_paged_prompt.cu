@@ -242,7 +242,9 @@ struct Joint {
   int last[2];
 };
 
-// 32 values of every row of a warp into shared memory (64-byte rows, 64-byte swizzle), in two buffers by turns.
+// 32 values of every row of a warp into shared memory (64-byte rows, 64-byte swizzle), in two buffers by turns.  Every
+// use of a buffer commits one bulk group, an empty one where no TMA store reads it, so that "all groups but the newest"
+// are those of this buffer's last use and before.
 __device__ __forceinline__ uint32_t stage_words(uint32_t stage, int d, const uint32_t* w) {
   const int lane = threadIdx.x & 31;
   const uint32_t buf = stage + (d / 32 & 1) * 2048;
@@ -268,7 +270,8 @@ __device__ __forceinline__ void store_rows(const CUtensorMap* tmO, int d, int he
   }
 }
 
-// Where some are not: four lanes write 64 bytes of a row.
+// Where some are not: four lanes write 64 bytes of a row.  The empty group keeps the count of stage_words: without it
+// the one group left pending could be a store of the job before that still reads the buffer written next.
 template <int HD>
 __device__ __forceinline__ void copy_rows(const PromptParams& p, const Job& job, int first, int log_pack, int row0, int d,
                                           uint32_t buf) {
@@ -286,6 +289,7 @@ __device__ __forceinline__ void copy_rows(const PromptParams& p, const Job& job,
       *reinterpret_cast<uint4*>(p.out + ((size_t)(job.q0 + to_tok) * p.n_heads + job.head0 + (row & ((1 << log_pack) - 1))) * HD + d +
                                 (lane & 3) * 8) = v;
   }
+  if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
 // The end of a tile's job where the usual one does not do: a tile that attends nothing; values to give back; the part of

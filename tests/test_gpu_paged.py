@@ -349,6 +349,32 @@ def test_prompt_chunks_repeat_bit_for_bit(tl):
     rig.ok()
 
 
+def _check_repeats(rig, q, cu, kv, times=30):
+    """One call against the oracle, then the same bits from `times` more."""
+    first, out = torch.full_like(q, float("nan")), torch.empty_like(q)
+    args = _i32(cu), _i32(kv)
+    rig.tl.paged_prompt_attn(rig.cache, 0, q, *args, first, seqs=_i32(rig.seqs))
+    rig.ok()
+    rig.check_prompt(0, q, cu, first, kv=kv)
+    for _ in range(times):
+        out.fill_(float("nan"))
+        rig.tl.paged_prompt_attn(rig.cache, 0, q, *args, out, seqs=_i32(rig.seqs))
+        assert torch.equal(out.view(torch.int16), first.view(torch.int16))
+    rig.ok()
+
+
+@pytest.mark.parametrize("hd,group,dtype", [(64, 4, FP16), (128, 4, BF16), (128, 1, FP16)])
+def test_prompt_full_blocks_before_a_few_rows_that_attend_nothing(tl, hd, group, dtype):
+    """Blocks whose rows are all stored at once, each followed by a lane of a few queries without positions: more blocks
+    than SMs, so that a CTA writes the one's outputs while the other's are still on their way."""
+    block = 256 // group
+    rig = Rig(tl, [block, 0], kv=1, group=group, hd=hd, page=16, dtype=dtype, layers=1)
+    new = [block, 3] * 200
+    rig.seqs = [0, 1] * 200
+    cu = np.cumsum([0] + new).tolist()
+    _check_repeats(rig, rig.queries(cu[-1]), cu, [block, 0] * 200)
+
+
 def test_prompt_skips_and_reports(tl):
     rig = Rig(tl, [40, 40, 40, 40], kv=1, group=1, hd=64, page=16, dtype=FP16)
     rig.cache.table[1, 2] = -1
