@@ -730,18 +730,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                        b + (uint64_t)(((k / 4) * (kStep * 128) + (k % 4) * 32) >> 4), kIdS, k != 0);
               mma_commit(&s_full[t][buf]);
             }
-            // the slot (after the last scores the queries too) is free once these products are done; at once
-            // where this tile attends neither
+            // the slot is free once these products are done (at once where this tile attends neither), the queries
+            // once all of this tile's scores are
             if (pv || qk)
               mma_commit(&empty[slot]);
             else
               mbar_arrive(&empty[slot]);
-            if (w == n - 1) {
-              if (qk)
-                mma_commit(&q_empty);
-              else
-                mbar_arrive(&q_empty);
-            }
+            if (w == n - 1) mma_commit(&q_empty);  // also where this turn has no scores: the last ones may still run
           }
           __syncwarp();
           issued = true;

@@ -375,6 +375,16 @@ def test_prompt_full_blocks_before_a_few_rows_that_attend_nothing(tl, hd, group,
     _check_repeats(rig, rig.queries(cu[-1]), cu, [block, 0] * 200)
 
 
+@pytest.mark.parametrize("hd,group,n", [(64, 2, 128), (128, 2, 128), (128, 1, 256), (64, 4, 97), (128, 2, 192)])
+def test_prompt_tiles_of_a_block_that_need_different_steps(tl, hd, group, n):
+    """The first tile's scores end before the second's and the next block's queries follow at once: many short blocks
+    a CTA, of different queries."""
+    rig = Rig(tl, [n], kv=1, group=group, hd=hd, page=32, dtype=FP16, layers=1)
+    lanes = 600 // -(-n * group // 256)
+    rig.seqs = [0] * lanes
+    _check_repeats(rig, rig.queries(n * lanes), list(range(0, n * lanes + 1, n)), [n] * lanes)
+
+
 def test_prompt_skips_and_reports(tl):
     rig = Rig(tl, [40, 40, 40, 40], kv=1, group=1, hd=64, page=16, dtype=FP16)
     rig.cache.table[1, 2] = -1
