@@ -783,12 +783,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int n = job.n;
         if (nj > 0 && !(good = __all_sync(0xffffffffu, wait_apart(&q_empty, (nj - 1) & 1, abort_p)))) break;
         if (n == 0) {
-          // q_full's and q_empty's phases go by jobs: an empty one passes its turn on
+          // q_full's and q_empty's phases go by jobs: an empty one passes its turn on.  `want` comes last: the product
+          // warps skip this phase of q_full, so it has to be over before there is a next job to wait for.
           if (lane == 0) {
-            mbar_arrive(&want);
             mbar_arrive(&q_full);
             mbar_arrive(&q_empty);
             mbar_arrive(&q_empty);
+            mbar_arrive(&want);
           }
         } else {
           if (lane == 0) {
