@@ -389,10 +389,10 @@ def test_prompt_tiles_of_a_block_that_need_different_steps(tl, hd, group, n):
 def test_prompt_lanes_without_positions_before_others(tl, empty):
     """Blocks that attend nothing, one to three in a row, then one with scores: the scores are of its own queries."""
     rig = Rig(tl, [0, 70], kv=1, group=2, hd=128, page=64, dtype=BF16, layers=1)
-    new = ([5] * empty + [70]) * 300
-    rig.seqs = ([0] * empty + [1]) * 300
+    new = ([5] * empty + [70]) * 250
+    rig.seqs = ([0] * empty + [1]) * 250
     cu = np.cumsum([0] + new).tolist()
-    _check_repeats(rig, rig.queries(cu[-1]), cu, ([0] * empty + [70]) * 300)
+    _check_repeats(rig, rig.queries(cu[-1]), cu, ([0] * empty + [70]) * 250)
 
 
 def test_prompt_skips_and_reports(tl):
