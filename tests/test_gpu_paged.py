@@ -395,6 +395,43 @@ def test_prompt_lanes_without_positions_before_others(tl, empty):
     _check_repeats(rig, rig.queries(cu[-1]), cu, ([0] * empty + [70]) * 250)
 
 
+def _sink(tl, n, dtype, split=0):
+    """One position of all the weight, n - 1 others 17.6 (natural units) below it, whose V alone is not zero."""
+    rig = Rig(tl, [n], kv=1, group=1, hd=64, page=128, dtype=dtype, layers=1, split=split, n_lanes=148)
+    rig.cache.k.zero_()
+    rig.cache.v.abs_().clamp_(max=1)      # of one sign: what is lost does not cancel
+    rig.cache.k[0, int(rig.table[0, 0]), 0, 0] = 2.2
+    rig.cache.v[0, int(rig.table[0, 0]), 0, 0] = 0
+    return rig
+
+
+def _check_sink(rig, got, q, n, least):
+    """The module's bound, with `least` in place of 2^-25: half the spacing of the smallest weights, relative to the
+    largest one."""
+    k, v = (paged_oracle.rows_of(p, rig.table[0], 0, n) for p in rig.pools(0))
+    want, mag, reach = paged_oracle.attend(_np(q), k, v, 0.125)
+    u = 2.0 ** -11 if rig.dtype == FP16 else 2.0 ** -8
+    e = 2.0 ** -21 + n * 2.0 ** -24 + 2 * 2.0 ** -23 * 64 * 0.125 * reach[:, None]
+    tol = u * np.abs(want) + mag * (u + e) * 1.01 + 2.0 ** -25 + n * least * np.nanmax(np.abs(v))
+    worst = (np.abs(_np(got) - want) / tol).max()
+    assert worst <= 1.0, f"{worst:.3g} of the tolerance"
+
+
+@pytest.mark.parametrize("lanes,dtype", [(1, FP16), (148, FP16), (148, BF16)])   # cut into pieces, and not
+def test_prompt_small_weights_behind_a_large_one(tl, lanes, dtype):
+    """The first step sets the base of the exponents, from which the weights of 60000 positions are small.  They are
+    held 2^7 times as large in FP16, spaced 2^-24 at the least: half of that is 2^-32 of the largest weight."""
+    n = 60000
+    rig = _sink(tl, n, dtype)
+    q = torch.ones((lanes, 1, 64), dtype=dtype, device="cuda")
+    out = torch.full_like(q, float("nan"))
+    lane = torch.zeros(lanes, dtype=torch.int32, device="cuda")
+    tl.paged_prompt_attn(rig.cache, 0, q, torch.arange(lanes + 1, dtype=torch.int32, device="cuda"), lane + n, out, seqs=lane)
+    rig.ok()
+    assert torch.equal(out, out[:1].expand_as(out))
+    _check_sink(rig, out[:1, 0], q[:1, 0], n, 2.0 ** -32)
+
+
 def test_prompt_skips_and_reports(tl):
     rig = Rig(tl, [40, 40, 40, 40], kv=1, group=1, hd=64, page=16, dtype=FP16)
     rig.cache.table[1, 2] = -1
