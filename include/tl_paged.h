@@ -12,7 +12,8 @@
  * Attention, per lane b and query head h (K/V head g = h / (n_heads / n_kv_heads)):
  *     out = sum_c softmax_c(scale * q . k_c) v_c      over the positions c the query attends
  * with the statistics and the sum in FP32; a query that attends nothing gives zeros.  The softmax
- * weights enter the second product rounded to the cache's 16-bit type, like the output.
+ * weights enter the second product rounded to the cache's 16-bit type, like the output: half a step,
+ * and in FP16 at least 2^-32 of the largest weight.
  *
  * Conventions are those of tl_storeh.h: caller-owned device memory on the current device,
  * asynchronous on a stream, host-side validation before any launch (a non-TL_OK return enqueues

@@ -18,8 +18,8 @@
 // one behind the other.
 //
 // Precision: scores, statistics and sums in FP32; p is rounded to the cache's type for the second
-// product (half a step, 2^-11 or 2^-8 relative, the rounding that the output itself has), its sum is
-// of the unrounded p.
+// product (half a step, 2^-11 or 2^-8 relative, the rounding that the output itself has, and in FP16 at
+// least 2^-40 of the split's largest), its sum is of the unrounded p.
 #include <cuda_bf16.h>
 
 #include "paged_internal.cuh"
@@ -33,6 +33,11 @@ constexpr int kDecThreads = 32 * kWarps;
 constexpr int kUnit = 16;       // positions a warp takes at a time
 constexpr int kRing = 96 << 10;  // shared memory of a CTA's rings: two CTAs per SM
 constexpr float kLog2e = 1.4426950408889634f;
+// FP16's exponents end soon: p is held 2^15 times as large (at most 2^15 of 65504), and the weights that FP16 spaces
+// 2^-24 apart are those below 2^-29 of the largest instead of 2^-14.  Sums and outputs carry the factor alike.  BF16 has
+// FP32's exponents and needs none.
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.0f : 15.0f;
 
 struct DecodeParams {
   PagedShape s;
@@ -285,6 +290,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Deco
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
         x = fmaxf(x, m[r]);
         const float base = x == -INFINITY ? 0.0f : x * p.scale2;  // nothing attended yet: every p is exp2(-inf) = 0
+        const float lift = kLift<BF16> - base;
         corr[r] = ex2(m[r] * p.scale2 - base);
         if (m[r] == x) corr[r] = 1.0f;
         m[r] = x;
@@ -293,7 +299,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Deco
         for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float e = ex2(fmaf(sc[nb][2 * r + j], p.scale2, -base));
+            const float e = ex2(fmaf(sc[nb][2 * r + j], p.scale2, lift));
             sc[nb][2 * r + j] = e;
             sum += e;
           }

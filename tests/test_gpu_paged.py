@@ -432,6 +432,18 @@ def test_prompt_small_weights_behind_a_large_one(tl, lanes, dtype):
     _check_sink(rig, out[:1, 0], q[:1, 0], n, 2.0 ** -32)
 
 
+@pytest.mark.parametrize("split,dtype", [(0, FP16), (4096, FP16), (4096, BF16)])
+def test_decode_small_weights_beside_a_large_one(tl, split, dtype):
+    """The same for the decode, whose FP16 weights are held 2^15 times as large: half a spacing is 2^-40."""
+    n = 60000
+    rig = _sink(tl, n, dtype, split)
+    q = torch.ones((1, 1, 64), dtype=dtype, device="cuda")
+    out = torch.full_like(q, float("nan"))
+    tl.paged_attn_decode(rig.cache, 0, q, _i32([n]), out)
+    rig.ok()
+    _check_sink(rig, out[:, 0], q[:, 0], n, 2.0 ** -40)
+
+
 def test_prompt_skips_and_reports(tl):
     rig = Rig(tl, [40, 40, 40, 40], kv=1, group=1, hd=64, page=16, dtype=FP16)
     rig.cache.table[1, 2] = -1
