@@ -96,6 +96,26 @@ __device__ __forceinline__ bool wait_apart(uint64_t* bar, uint32_t parity, volat
   return mbar_try_wait(bar, parity) || wait_on(bar, parity, abort);
 }
 
+// For a wait that may span any number of jobs: the limit starts anew with each job that the CTA takes.
+__device__ __noinline__ bool wait_over_jobs(uint64_t* bar, uint32_t parity, volatile int* abort, volatile const int* taken) {
+  int seen = *taken;
+  long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort) return false;
+    const int now = *taken;
+    const long long t = clock64();
+    if (now != seen) {
+      seen = now;
+      t0 = t;
+    }
+    if (t - t0 > kPWait) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
 struct PromptParams {
   PagedShape s;
   const uint16_t* v;  // the layer's
@@ -499,7 +519,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   __shared__ uint32_t tmem_base;
   __shared__ uint64_t want, go;
   __shared__ Dirty dirt;
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, jobs_taken;
   __shared__ Joint joint_mem;
   Joint* joint = &joint_mem;
   __shared__ Job jobs[2];
@@ -533,6 +553,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&job_empty[t], 12);  // warps that read a job
     }
     abort_flag = 0;
+    jobs_taken = 0;
     mbar_fence_init();
   }
   pdl_wait();
@@ -949,6 +970,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (nj >= 2 && !(good = __all_sync(0xffffffffu, wait_apart(&job_empty[nj & 1], ((nj >> 1) - 1) & 1, abort_p)))) break;
         if (lane == 0) {
           jobs[nj & 1] = job;
+          *(volatile int*)&jobs_taken = nj + 1;
           mbar_arrive(&job_full[nj & 1]);
         }
         __syncwarp();
@@ -956,7 +978,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     } else if (warp > 12) {
       // ------------------------------------------------------------ cleaning, with warp 9
-      for (int g = 0; wait_apart(&go, g & 1, abort_p); ++g) {
+      // (a lane's single query behind whole steps leaves nothing to clean, in a call of seconds too)
+      for (int g = 0; wait_over_jobs(&go, g & 1, abort_p, &jobs_taken); ++g) {
         const Dirty d = dirt;
         if (d.slot < 0) break;
         clean_step<HD, BF16>(vs + d.slot * Smem::kKv, d, warp - 12);

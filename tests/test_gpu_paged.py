@@ -444,6 +444,27 @@ def test_decode_small_weights_beside_a_large_one(tl, split, dtype):
     _check_sink(rig, out[:, 0], q[:, 0], n, 2.0 ** -40)
 
 
+def test_prompt_call_of_seconds_with_nothing_to_clean(tl):
+    """A thousand single queries over 2^22 positions each (eight pages, entered over and over): the warps that clean V
+    wait for the whole call, which is no reason to give up.  Every position counts as often as the others, so the
+    result is that of the eight pages once."""
+    kv, hd, page, lanes, n = 16, 64, 128, 1024, 1 << 22
+    cache = tl.PagedCache(tl.PagedDesc(1, 8, page, kv, hd, 1, n // page, tl.TL_KV_FP16), kv, 1)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    for pool in (cache.k, cache.v):
+        pool.copy_(torch.randn(pool.shape, generator=g, device="cuda"))
+    cache.table[0] = torch.arange(n // page, device="cuda") % 8
+    q = torch.randn((1, kv, hd), generator=g, device="cuda").to(FP16).expand(lanes, kv, hd).contiguous()
+    out = torch.full_like(q, float("nan"))
+    lane = torch.zeros(lanes, dtype=torch.int32, device="cuda")
+    cu = torch.arange(lanes + 1, dtype=torch.int32, device="cuda")
+    tl.paged_prompt_attn(cache, 0, q, cu, lane + n, out, seqs=lane)
+    assert tl.poll_status(cache) == tl.TL_OK
+    res = paged_oracle.decode(_np(cache.k[0]), _np(cache.v[0]), np.arange(8)[None], _np(q[:1]), [8 * page], [0], hd ** -0.5)
+    _check(out[:1], res, FP16, hd, hd ** -0.5, n, float(cache.v.abs().max()))
+    assert torch.equal(out[:-lanes // 8], out[:1].expand(lanes - lanes // 8, kv, hd))   # the last blocks are cut into pieces
+
+
 def test_prompt_skips_and_reports(tl):
     rig = Rig(tl, [40, 40, 40, 40], kv=1, group=1, hd=64, page=16, dtype=FP16)
     rig.cache.table[1, 2] = -1
