@@ -181,9 +181,10 @@ TL_API tl_status tl_paged_fork(const tl_paged_desc* desc, tl_paged_cache cache, 
  * sequence is replaced by a free page, with a copy of its rows where the page begins before
  * ctx_len[i].  Every listed sequence that shares such a page gets its own.  Sequences are served
  * in the order of the list while the free pages last; the first one that they do not cover and
- * all behind it get nothing, and TL_ERR_DEVICE_CAPACITY is recorded.  A sequence that is out of
- * range, stands in the list before, has a negative length, or whose positions do not fit its
- * table row gets nothing, and TL_ERR_DEVICE_RANGE is recorded. */
+ * all behind it get nothing, and TL_ERR_DEVICE_CAPACITY is recorded (tl_storeh_poll_status returns
+ * it before a TL_ERR_DEVICE_RANGE, such as that of an append to the missing pages).  A sequence that
+ * is out of range, stands in the list before, has a negative length, or whose positions do not fit
+ * its table row gets nothing, and TL_ERR_DEVICE_RANGE is recorded. */
 TL_API tl_status tl_paged_reserve(const tl_paged_desc* desc, tl_paged_cache cache, const int32_t* seqs,
                                   const int32_t* ctx_len, const int32_t* n_new, int32_t n, void* workspace,
                                   size_t workspace_bytes, tl_stream_t stream);

@@ -407,11 +407,14 @@ TL_API tl_status tl_storeh_attn_decode_static_ws(const tl_storeh_desc* desc, tl_
  * of tl_storeh_attn_decode record in `workspace`.  Returns TL_OK,
  * TL_ERR_DEVICE_TIMEOUT (a bounded device wait gave up), TL_ERR_DEVICE_RANGE
  * (a lane's loops/ctx_len was out of range and the lane was skipped),
- * TL_ERR_DEVICE_CAPACITY (a paged cache ran out of free pages) or TL_ERR_CUDA.  The status word starts at the beginning of the workspace,
+ * TL_ERR_DEVICE_CAPACITY (a paged cache ran out of free pages) or TL_ERR_CUDA.
+ * Where several were recorded, a timeout comes first and clears the others; a
+ * lack of pages comes before what was out of range, which the next call then
+ * returns.  The status word starts at the beginning of the workspace,
  * whose first 256 bytes are reserved for it; a freshly allocated workspace
  * must have those 256 bytes zero-filled once (or be cleared with this call)
  * before its first use.  When the word is not zero this call clears all 256
- * bytes.
+ * bytes (but for what is left for the next call).
  */
 TL_API tl_status tl_storeh_poll_status(void* workspace, size_t workspace_bytes, tl_stream_t stream);
 

@@ -429,7 +429,8 @@ def residual_norm_check(residual, threshold: float, it: int, loops, abort_flags,
 
 def poll_status(cache, stream=None) -> int:
     """Synchronise and return (and clear) the device status of a workspace: a StoreHCache's,
-    a DeltaCache's made with n_lanes, a PagedCache's, or a workspace tensor of its own (verification, prefill)."""
+    a DeltaCache's made with n_lanes, a PagedCache's, or a workspace tensor of its own (verification, prefill).
+    TL_ERR_DEVICE_CAPACITY leaves a TL_ERR_DEVICE_RANGE that was recorded beside it for the next call."""
     if isinstance(cache, PagedCache):
         import torch
         with torch.cuda.device(cache.device):

@@ -480,13 +480,17 @@ tl_status tl_storeh_poll_status(void* workspace, size_t workspace_bytes, tl_stre
   if (e == cudaSuccess) e = cudaStreamSynchronize(cs);
   if (e != cudaSuccess) return cuda_fail(e, "reading the status word");
   if (word != 0) {
+    // one kind a call: out of range stays for the next one where the lack of pages is reported
+    static_assert(tl::kStatusRange == 1, "the word's first byte, with the rest 0");
+    const bool range_left = (word & tl::kStatusFull) && (word & tl::kStatusRange) && !(word & tl::kStatusTimeout);
     e = cudaMemsetAsync(workspace, 0, 256, cs);  // the status block
+    if (e == cudaSuccess && range_left) e = cudaMemsetAsync(workspace, 1, 1, cs);
     if (e == cudaSuccess) e = cudaStreamSynchronize(cs);
     if (e != cudaSuccess) return cuda_fail(e, "clearing the status word");
   }
   if (word & tl::kStatusTimeout) return fail(TL_ERR_DEVICE_TIMEOUT, "device status word 0x%x", word);
-  if (word & tl::kStatusRange) return fail(TL_ERR_DEVICE_RANGE, "device status word 0x%x", word);
   if (word & tl::kStatusFull) return fail(TL_ERR_DEVICE_CAPACITY, "device status word 0x%x", word);
+  if (word & tl::kStatusRange) return fail(TL_ERR_DEVICE_RANGE, "device status word 0x%x", word);
   return TL_OK;
 }
 

@@ -598,6 +598,22 @@ def test_pages_refusals(tl):
     t.do("reserve", [4, 1], [0, 0], [128, 1])
 
 
+def test_poll_tells_a_lack_of_pages_and_what_was_out_of_range(tl):
+    """Both recorded, by one call or by a step of two: each is returned once, the lack of pages first."""
+    c = tl.PagedCache(tl.PagedDesc(1, 3, 16, 1, 64, 4, 4), 1, 4)
+    x = torch.zeros((2, 1, 64), dtype=FP16, device="cuda")
+    polls = lambda: [tl.poll_status(c) for _ in range(3)]  # noqa: E731
+    tl.paged_reserve(c, _i32([9, 0, 1]), _i32([0, 0, 0]), _i32([1, 32, 32]))
+    assert polls() == [tl.TL_ERR_DEVICE_CAPACITY, tl.TL_ERR_DEVICE_RANGE, tl.TL_OK]
+    tl.paged_reserve(c, _i32([1, 2]), _i32([0, 0]), _i32([16, 16]))      # sequence 2 gets no page for its token
+    tl.paged_append(c, 0, x, x, _i32([0, 0]), seqs=_i32([1, 2]))
+    assert polls() == [tl.TL_ERR_DEVICE_CAPACITY, tl.TL_ERR_DEVICE_RANGE, tl.TL_OK]
+    tl.paged_reserve(c, _i32([2]), _i32([0]), _i32([16]))
+    assert polls() == [tl.TL_ERR_DEVICE_CAPACITY, tl.TL_OK, tl.TL_OK]
+    tl.paged_append(c, 0, x, x, _i32([0, 0]), seqs=_i32([1, 2]))
+    assert polls() == [tl.TL_ERR_DEVICE_RANGE, tl.TL_OK, tl.TL_OK]
+
+
 @pytest.mark.parametrize("n_pages,max_pages", [(20001, 400), (40000, 3000)])
 def test_pages_at_size(tl, n_pages, max_pages):
     """Several scan rounds over the pool and over the candidates of one call, odd sizes, random lists."""
