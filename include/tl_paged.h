@@ -99,7 +99,8 @@ TL_API tl_status tl_paged_workspace_bytes(const tl_paged_desc* desc, int32_t n_h
  * No two rows of a call may go to the same position.
  * A row whose sequence or position is out of range, whose page is not in the table, or whose page
  * is held by more than one sequence (refs > 1: tl_paged_reserve gives the writer its own) is not
- * written, and TL_ERR_DEVICE_RANGE is recorded.
+ * written, nor are the rows of a lane that begins before row 0, ends before it begins or ends past
+ * n_rows; TL_ERR_DEVICE_RANGE is recorded.
  * Errors: TL_ERR_INVALID_ARG, TL_ERR_CAPACITY (layer, n_lanes > max_seqs without seqs, workspace),
  * TL_ERR_UNSUPPORTED, TL_ERR_CUDA.
  */

@@ -56,8 +56,10 @@ __global__ void __launch_bounds__(kAppendThreads)
     }
     const int b = cu_rows ? find_lane(cu_rows, n_lanes, r, lane) : r;
     const int seq = seqs ? seqs[b] : b;
-    const long long pos = (long long)start_pos[b] + (cu_rows ? r - cu_rows[b] : 0);
+    const int own0 = cu_rows ? cu_rows[b] : r, own1 = cu_rows ? cu_rows[b + 1] : r + 1;  // the lane's rows
+    const long long pos = (long long)start_pos[b] + r - own0;
     bool ok = seq >= 0 && seq < s.max_seqs && pos >= 0 && pos < s.max_len();
+    ok = ok && own0 >= 0 && own0 <= r && r < own1 && own1 <= n_rows;
     int page = -1;
     if (ok) page = c.table[(size_t)seq * s.max_pages + (int)(pos >> log_page)];
     ok = ok && page >= 0 && page < s.n_pages;
@@ -73,6 +75,10 @@ __global__ void __launch_bounds__(kAppendThreads)
       if (at < chunks) *reinterpret_cast<uint4*>(dst + (size_t)(at >> log_head) * s.block_elems() + (at & ((1 << log_head) - 1)) * 8) = x[i];
     }
   }
+  // a lane may claim rows that no warp above has met: one block looks the lanes over
+  if (cu_rows && blockIdx.x == 0 && blockIdx.y == 0)
+    for (int b = threadIdx.x; b < n_lanes; b += kAppendThreads)
+      if (cu_rows[b] < 0 || cu_rows[b + 1] < cu_rows[b] || cu_rows[b + 1] > n_rows) atomicOr(status, kStatusRange);
 }
 
 }  // namespace

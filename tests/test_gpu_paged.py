@@ -147,6 +147,30 @@ def test_append_skips_what_it_may_not_write(tl):
     assert torch.equal(rig.cache.k.view(torch.int16), want.view(torch.int16))
 
 
+@pytest.mark.parametrize("cu,written", [
+    ([0, 3, 8, 8], (0,)),             # lane 1 claims rows that there are not
+    ([0, 3, 6, 9], (0, 1)),           # lane 2 has none of its rows
+    ([-2, 2, 4, 6], (1, 2)),          # lane 0 begins before the first row
+    ([0, 4, 2, 6], ()),               # lane 1 ends before it begins: rows 2 and 3 have two owners
+])
+def test_append_reports_lanes_whose_rows_are_out_of_range(tl, cu, written):
+    """Such a lane's rows are not written, the other lanes' are, and the call reports it."""
+    rig = Rig(tl, [20, 20, 20], kv=2, group=1, hd=64, page=16, dtype=FP16)
+    x = torch.randn((6, 2, 64), generator=rig.g, device="cuda").to(FP16)
+    before = rig.cache.k.clone()
+    tl.paged_append(rig.cache, 0, x, x, _i32([2, 2, 2]), cu_rows=_i32(cu))
+    assert tl.poll_status(rig.cache) == tl.TL_ERR_DEVICE_RANGE
+    same = lambda a, b: torch.equal(a.view(torch.int16), b.view(torch.int16))  # noqa: E731
+    for b in range(3):
+        for i in range(max(0, min(6, cu[b + 1]) - cu[b])):
+            at = (0, int(rig.table[b, 0]), slice(None), 2 + i)
+            if b in written:
+                assert same(rig.cache.k[at], x[cu[b] + i])
+            elif written:
+                assert same(rig.cache.k[at], before[at])
+    assert same(rig.cache.k[1], before[1])
+
+
 # ---------------------------------------------------------------------------------------- decode
 @pytest.mark.parametrize("kv,group,hd,page,dtype,lens,split", [
     (4, 1, 128, 16, FP16, [0, 1, 15, 16, 17, 63, 64, 65], 0),
