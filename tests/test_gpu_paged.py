@@ -506,6 +506,33 @@ def test_prompt_skips_and_reports(tl):
         assert tl.poll_status(rig.cache) == tl.TL_ERR_DEVICE_RANGE
 
 
+@pytest.mark.parametrize("cu", [[0, 40, 30, 120, 161], [-1, 40, 80, 120, 160], [0, 40, 80, 70, 160], [5, 45, 200, 60, 90]])
+@pytest.mark.parametrize("group,hd", [(1, 64), (8, 128)])
+def test_prompt_lanes_whose_rows_are_out_of_range(tl, cu, group, hd):
+    """A lane that begins before row 0, ends before it begins or ends past the rows is skipped: the rows of no other
+    lane stay as they were, and those of one other lane alone are its results."""
+    rows, lens = 160, [30, 40, 60, 100]
+    rig = Rig(tl, lens, kv=1, group=group, hd=hd, page=16, dtype=FP16)
+    q = rig.queries(rows)
+    out = torch.full_like(q, float("nan"))
+    tl.paged_prompt_attn(rig.cache, 0, q, _i32(cu), _i32(lens), out)
+    assert tl.poll_status(rig.cache) == tl.TL_ERR_DEVICE_RANGE
+    valid = [b for b in range(4) if 0 <= cu[b] <= cu[b + 1] <= rows]
+    owners = np.zeros(rows, int)
+    for b in valid:
+        owners[cu[b]:cu[b + 1]] += 1
+    assert 0 < len(valid) < 4
+    assert torch.isnan(out[torch.from_numpy(owners == 0)]).all()
+    for b in valid:
+        mine = np.arange(cu[b], cu[b + 1])
+        alone = owners[mine] == 1
+        k, v = (paged_oracle.rows_of(p, rig.table[b], 0, lens[b]) for p in rig.pools(0))
+        last = lens[b] - len(mine) + np.arange(len(mine))
+        for h in range(group):
+            res = paged_oracle.attend(_np(q)[mine, h], k, v, hd ** -0.5, last)
+            _check(_np(out)[mine, h][alone], [r[alone] for r in res], FP16, hd, hd ** -0.5, lens[b], rig.vmax(0))
+
+
 def test_prompt_row_equals_decode_of_the_same_position(tl):
     """The last row of a prompt and the decode of its token agree within the roundings of both."""
     lens = [500, 77]
