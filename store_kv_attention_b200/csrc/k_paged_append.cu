@@ -6,7 +6,7 @@
 // One warp takes 2 KB of K or of V of one row, so that a lane has four 16-byte loads in flight and a
 // 48-token call still spreads over as many warps as it has parts.  Measured: 24 packed prompts of up to 2048
 // rows of 8 x 128, 204 MB in 34.5 us a call, 5.9 TB/s (0.91 of a copy's bandwidth; at 32 registers, twice the warps,
-// 37.3); 48 tokens 5.3 us.
+// 37.3); 48 tokens 6.5 us a call, most of it the host's.
 #include "paged_internal.cuh"
 #include "tc_ptx.cuh"
 
